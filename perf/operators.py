@@ -1,0 +1,369 @@
+"""The feature-row operators' cases: what one pass of each reads and computes, and its plain form.
+
+Three operators around the sparse convolution's training step, on (rows, channels) features:
+
+* embed: a row's features from its token id (lookup in a table, times a scale), and the table's
+  gradient, summed by sorted tokens;
+* norm: root-mean-square norm with the residual's addition, rows out in their own type and / or
+  in 8 bits, and its backward pass, from rows or from 8-bit rows;
+* q8: activation checkpoints in 8 bits (e4m3 values, one power-of-two scale per 32 channels of a
+  row), written and read back, and the convolution's weight gradient from them.
+
+8-bit rows are returned as the values they stand for, in bf16, which holds them exactly.
+"""
+import math
+
+import torch
+
+own = False
+
+DTYPES = {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}
+GROUP = 32       # channels that share a scale
+EPS = 1e-6
+NO_TOKEN = -1    # the id of a row without a token
+OFFSETS = [(a, b, c) for a in (-1, 0, 1) for b in (-1, 0, 1) for c in (-1, 0, 1)]
+
+
+# ----------------------------------------------------------------------------- cases
+def listed():
+    return [
+        # a few rows looked up while serving: nothing but latency
+        {"name": "embed_fwd_few", "op": "embed_fwd", "n": 8, "vocab": 32000, "c": 1024, "dtype": "f16", "ids": 64},
+        # a long batch of tokens into wide rows, from a large vocabulary
+        {"name": "embed_fwd_batch", "op": "embed_fwd", "n": 32768, "vocab": 131072, "c": 4096, "dtype": "bf16", "ids": 64},
+        # 500k voxels with a categorical code each (the 4 x 125k LiDAR training step's rows)
+        {"name": "embed_wgrad_voxels", "op": "embed_wgrad", "n": 500000, "vocab": 1000, "c": 128, "dtype": "bf16", "ids": 32},
+        # a training step's tokens, odd counts: most of the table's rows get no gradient
+        {"name": "embed_wgrad_tokens", "op": "embed_wgrad", "n": 16383, "vocab": 50257, "c": 1024, "dtype": "f16", "ids": 64},
+        # four rows between two layers while serving
+        {"name": "norm_fwd_few", "op": "norm_fwd", "n": 4, "c": 4096, "dtype": "bf16", "res": True, "out": "8bit"},
+        # the training step's rows: the residual's addition, rows for the convolution, 8 bits for its backward pass
+        {"name": "norm_fwd_voxels", "op": "norm_fwd", "n": 500000, "c": 128, "dtype": "bf16", "res": True, "out": "both"},
+        # wide rows in 32 bits, an odd count, no residual
+        {"name": "norm_fwd_wide", "op": "norm_fwd", "n": 8191, "c": 8192, "dtype": "f32", "res": False, "out": "rows"},
+        # the training step's backward pass from the 8-bit checkpoint, the residual stream's gradient added
+        {"name": "norm_bwd_voxels", "op": "norm_bwd", "n": 500000, "c": 128, "dtype": "bf16", "dh": True, "saved": "8bit"},
+        # wide rows in 16 bits kept whole
+        {"name": "norm_bwd_wide", "op": "norm_bwd", "n": 4097, "c": 5120, "dtype": "f16", "dh": False, "saved": "rows"},
+        # the 2 x 100k LiDAR layer's rows into a checkpoint and back
+        {"name": "q8_rows", "op": "q8_rows", "n": 200000, "c": 64, "dtype": "f16"},
+        # weight gradient of the 2,000-voxel layer from its checkpoint: latency
+        {"name": "q8_wgrad_small", "op": "q8_wgrad", "n": 2000, "cin": 16, "cout": 16, "dtype": "f32", "batch": 1, "grid": 32},
+        # weight gradient of the 4 x 125k LiDAR training step from its checkpoint
+        {"name": "q8_wgrad_train", "op": "q8_wgrad", "n": 500000, "cin": 128, "cout": 128, "dtype": "bf16", "batch": 4, "grid": 1440},
+    ]
+
+
+def _log(rng, lo, hi):
+    return max(lo, min(hi, int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))))
+
+
+def _channels(rng, lo, hi):
+    return 8 * _log(rng, lo // 8, hi // 8)
+
+
+def draw(rng):
+    op = rng.choice(["embed_fwd", "embed_wgrad", "norm_fwd", "norm_bwd", "q8_rows", "q8_wgrad"])
+    dtype = rng.choice(["f32", "f16", "bf16"])
+    if op in ("embed_fwd", "embed_wgrad"):
+        c = _channels(rng, 8, 8192)
+        n = _log(rng, 1, min(500000, (1 << 26) // c))
+        vocab = _log(rng, 1, min(262144, (1 << 26) // c))
+        return {"op": op, "n": n, "vocab": vocab, "c": c, "dtype": dtype, "ids": rng.choice([32, 64])}
+    if op == "q8_wgrad":
+        if dtype != "f32" and rng.random() < 0.7:
+            cin, cout = rng.choice([64, 128]), rng.choice([64, 128])
+            n = _log(rng, 100, 400000)
+        else:
+            cin, cout = _channels(rng, 8, 64), _channels(rng, 8, 64)
+            n = _log(rng, 100, 60000)
+        batch = rng.choice([1, 2, 4])
+        grid = max(8, int((n / batch) ** (1 / 3) * rng.uniform(2.0, 6.0)))
+        return {"op": op, "n": n, "cin": cin, "cout": cout, "dtype": dtype, "batch": batch, "grid": grid}
+    c = _channels(rng, 8, 16384)
+    n = _log(rng, 1, min(500000, (1 << 25) // c))
+    if op == "q8_rows":
+        return {"op": op, "n": n, "c": c, "dtype": dtype}
+    if op == "norm_fwd":
+        return {"op": op, "n": n, "c": c, "dtype": dtype, "res": rng.random() < 0.5, "out": rng.choice(["rows", "8bit", "both"])}
+    return {"op": op, "n": n, "c": c, "dtype": dtype, "dh": rng.random() < 0.5, "saved": rng.choice(["rows", "8bit"])}
+
+
+# ----------------------------------------------------------------------------- inputs
+def _ids(g, n, vocab, bits):
+    """Token ids whose frequencies fall off as 1 / rank, the ranks spread over the vocabulary; 1 in 32 rows has none."""
+    rank = torch.exp(torch.rand(n, generator=g, device="cuda", dtype=torch.float64) * math.log(vocab + 1)).long() - 1
+    ids = torch.randperm(vocab, generator=g, device="cuda")[rank.clamp_(0, vocab - 1)]
+    ids[torch.rand(n, generator=g, device="cuda") < 1 / 32] = NO_TOKEN
+    return ids.to(torch.int32 if bits == 32 else torch.int64)
+
+
+def _voxels(g, n, batch, grid):
+    """n distinct (batch, x, y, z) rows in random order: 60% on a two-cell ground layer, the rest in Gaussian clusters, as a scan has them."""
+    dims = (grid, grid, 41 if grid > 100 else grid)
+    m, at = 2 * n + 64, lambda *s: torch.rand(*s, generator=g, device="cuda")  # noqa: E731
+    ground = at(m) < 0.6
+    centre = at(200, 3)[torch.randint(0, 200, (m,), generator=g, device="cuda")]
+    xyz = [torch.where(ground, at(m) * d, (centre[:, i] * d + 8.0 * torch.randn(m, generator=g, device="cuda"))).floor().long()
+           for i, d in enumerate(dims)]
+    xyz[2] = torch.where(ground, 2 + (at(m) < 0.5).long(), xyz[2])
+    fill = torch.randint(0, batch * dims[0] * dims[1] * dims[2], (m,), generator=g, device="cuda")
+    b = torch.randint(0, batch, (m,), generator=g, device="cuda")
+    cell = ((b * dims[0] + xyz[0]) * dims[1] + xyz[1]) * dims[2] + xyz[2]
+    inside = torch.stack([(x >= 0) & (x < d) for x, d in zip(xyz, dims)]).all(0)
+    cell = torch.unique(cell[inside])
+    cell = cell[torch.randperm(len(cell), generator=g, device="cuda")][:n]
+    if len(cell) < n:  # a small grid: filled up with cells anywhere
+        more = torch.unique(torch.cat([fill, torch.arange(min(4 * n + 64, batch * dims[0] * dims[1] * dims[2]), device="cuda")]))
+        more = more[~torch.isin(more, cell)]
+        cell = torch.cat([cell, more[torch.randperm(len(more), generator=g, device="cuda")][:n - len(cell)]])
+        cell = cell[torch.randperm(len(cell), generator=g, device="cuda")]
+    z, y, x, b = cell % dims[2], cell // dims[2] % dims[1], cell // (dims[2] * dims[1]) % dims[0], cell // (dims[2] * dims[1] * dims[0])
+    return torch.stack([b, x, y, z], 1).to(torch.int32).contiguous()
+
+
+def _pairs(coords):
+    """Per offset of a 3^3 submanifold convolution: the input rows and the output rows of its pairs."""
+    c = coords.long()
+    key = lambda v: ((v[:, 0] * 4096 + v[:, 1] + 1) * 4096 + v[:, 2] + 1) * 4096 + v[:, 3] + 1  # noqa: E731
+    keys, rows = torch.sort(key(c))
+    found = []
+    for d in OFFSETS:
+        k = key(c + torch.tensor((0,) + d, device="cuda"))
+        at = torch.searchsorted(keys, k).clamp_(max=len(keys) - 1)
+        out = (keys[at] == k).nonzero()[:, 0]
+        found.append((rows[at[out]], out))
+    return found
+
+
+def prepare(case, seed):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed * 1000003 + 17)
+    op, dt = case["op"], DTYPES[case["dtype"]]
+    normal = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
+    s = {"case": case, "op": op}
+    if op in ("embed_fwd", "embed_wgrad"):
+        s["ids"] = _ids(g, case["n"], case["vocab"], case["ids"])
+        s["scale"] = math.sqrt(case["c"])
+        if op == "embed_fwd":
+            s["table"] = (normal(case["vocab"], case["c"]) / s["scale"]).to(dt)
+        else:
+            s["dy"] = normal(case["n"], case["c"]).to(dt)
+    elif op == "norm_fwd":
+        n, c = case["n"], case["c"]
+        s["x"] = normal(n, c).to(dt)
+        s["res"] = (2 * normal(n, c)).to(dt) if case["res"] else None
+        s["w"] = (1 + 0.2 * normal(c)).to(dt)
+    elif op == "norm_bwd":
+        n, c = case["n"], case["c"]
+        h = (2 * normal(n, c)).to(dt)
+        s["rstd"] = torch.rsqrt(h.float().square().mean(1) + EPS)
+        s["h"] = h if case["saved"] == "rows" else _encode(h.float())
+        s["dy"] = normal(n, c).to(dt)
+        s["dh"] = normal(n, c).to(dt) if case["dh"] else None
+        s["w"] = (1 + 0.2 * normal(c)).to(dt)
+    elif op == "q8_rows":
+        # rows of an activation: some channels much larger than the rest
+        s["x"] = (normal(case["n"], case["c"]) * torch.exp(normal(case["c"]))).to(dt)
+    else:
+        coords = _voxels(g, case["n"], case["batch"], case["grid"])
+        s["xq"] = _encode(normal(case["n"], case["cin"]).to(dt).float())
+        s["dy"] = normal(case["n"], case["cout"]).to(dt)
+        s["pairs"] = _pairs(coords)
+    if own:  # the handles that a user's program keeps: a checkpoint as the forward pass left it, the layer's kernel map, a workspace
+        import sparse_convolution_voxel_b200 as scv
+        s["ws"] = scv.Workspace()
+        if op == "norm_bwd" and case["saved"] == "8bit":
+            s["h"] = scv.Q8Rows(*s["h"])
+        if op == "q8_wgrad":
+            s["xq"] = scv.Q8Rows(*s["xq"])
+            s["map"] = scv.kernel_map(scv.hash_table(coords), len(coords), coords, scv.subm_geom(3), s["ws"])
+    return s
+
+
+# ----------------------------------------------------------------------------- plain forms
+def _encode(v):
+    """8-bit rows of v (32 bits): e4m3 values and, per row and 32 channels, the exponent byte of the smallest power of two
+    (at least 2^-126) that brings the largest finite magnitude to 448 or less. What is not finite becomes NaN."""
+    n, c = v.shape
+    groups = -(-c // GROUP)
+    fine = torch.isfinite(v)
+    big = torch.zeros(n, groups * GROUP, device=v.device)
+    big[:, :c] = torch.where(fine, v.abs(), 0.0)
+    bits = big.view(n, groups, GROUP).amax(2).view(torch.int32)
+    e = (((bits + 0x1FFFFF) >> 23) - 8).clamp_(min=1)
+    inverse = ((254 - e) << 23).view(torch.float32)
+    q = torch.where(fine, v * inverse.repeat_interleave(GROUP, 1)[:, :c], torch.nan)
+    return q.to(torch.float8_e4m3fn), e.to(torch.uint8)
+
+
+def _decode(q, e):
+    """The values of 8-bit rows, in 32 bits."""
+    scale = (e.int() << 23).view(torch.float32)
+    return q.float() * scale.repeat_interleave(GROUP, 1)[:, :q.shape[1]]
+
+
+def _plain(s):
+    case, op, dt = s["case"], s["op"], DTYPES[s["case"]["dtype"]]
+    if op == "embed_fwd":
+        have = s["ids"] != NO_TOKEN
+        rows = s["table"][torch.where(have, s["ids"], 0).long()].float() * s["scale"]
+        return torch.where(have[:, None], rows, 0.0).to(dt)
+    if op == "embed_wgrad":
+        have = (s["ids"] != NO_TOKEN).nonzero()[:, 0]
+        out = torch.zeros(case["vocab"], case["c"], device="cuda")
+        return out.index_add_(0, s["ids"][have].long(), s["dy"][have].float()) * s["scale"]
+    if op == "norm_fwd":
+        h = s["x"].float() + s["res"].float() if case["res"] else s["x"].float()
+        rstd = torch.rsqrt((h * h).mean(1) + EPS)
+        y = h * rstd[:, None] * s["w"].float()
+        out = {"rstd": rstd}
+        if case["res"]:
+            out["h"] = h.to(dt)
+        if case["out"] != "8bit":
+            out["y"] = y.to(dt)
+        if case["out"] != "rows":
+            out["y8"] = _decode(*_encode(y)).to(torch.bfloat16)
+        return out
+    if op == "norm_bwd":
+        h = s["h"].float() if case["saved"] == "rows" else _decode(*s["h"])
+        dy, rstd = s["dy"].float(), s["rstd"][:, None]
+        at = h * rstd
+        g = dy * s["w"].float()
+        dx = rstd * (g - at * (g * at).mean(1, keepdim=True))
+        if case["dh"]:
+            dx = dx + s["dh"].float()
+        return {"dx": dx.to(dt), "dw": (dy * at).sum(0)}
+    if op == "q8_rows":
+        return _decode(*_encode(s["x"].float())).to(torch.bfloat16)
+    x, dy = _decode(*s["xq"]), s["dy"].float()
+    dw = [x[i].t() @ dy[j] for i, j in s["pairs"]]
+    return torch.stack(dw)
+
+
+def _own(s):
+    import sparse_convolution_voxel_b200 as scv
+    case, op = s["case"], s["op"]
+    if op == "embed_fwd":
+        return scv.embed_fwd(s["ids"], s["table"], s["scale"], pad_id=NO_TOKEN)
+    if op == "embed_wgrad":
+        return scv.embed_wgrad(s["ids"], s["dy"], case["vocab"], s["scale"], pad_id=NO_TOKEN, ws=s["ws"])
+    if op == "norm_fwd":
+        r = scv.rms_norm_fwd(s["x"], s["w"], s["res"], EPS, rows=case["out"] != "8bit", q8=case["out"] != "rows")
+        out = {"rstd": r.rstd}
+        if case["res"]:
+            out["h"] = r.h
+        if case["out"] != "8bit":
+            out["y"] = r.y
+        if case["out"] != "rows":
+            out["y8"] = scv.q8_unpack(r.y8, torch.bfloat16)
+        return out
+    if op == "norm_bwd":
+        dx, dw = scv.rms_norm_bwd(s["dy"], s["h"], s["rstd"], s["w"], s["dh"], ws=s["ws"])
+        return {"dx": dx, "dw": dw}
+    if op == "q8_rows":
+        return scv.q8_unpack(scv.q8_pack(s["x"]), torch.bfloat16)
+    return scv.conv_wgrad_q8(s["xq"], s["dy"], s["map"], ws=s["ws"])
+
+
+def run(state):
+    return _own(state) if own else _plain(state)
+
+
+# ----------------------------------------------------------------------------- work
+def _q8_bytes(n, c):
+    return n * c + n * -(-c // GROUP)
+
+
+def work(case):
+    op, e = case["op"], 4 if case["dtype"] == "f32" else 2
+    if op in ("embed_fwd", "embed_wgrad"):
+        n, c, vocab = case["n"], case["c"], case["vocab"]
+        ids = n * case["ids"] // 8
+        if op == "embed_fwd":
+            return {"bytes": ids + n * c * e + min(n, vocab) * c * e, "flops": n * c}
+        return {"bytes": ids + n * c * e + vocab * c * 4, "flops": n * c}
+    if op == "q8_wgrad":
+        n, cin, cout = case["n"], case["cin"], case["cout"]
+        pairs = int(1.35 * n)  # the centre of every row, and a third of a neighbour
+        return {"bytes": _q8_bytes(n, cin) + n * cout * e + 8 * pairs + 4 * 27 * cin * cout, "flops": 2 * pairs * cin * cout}
+    n, c = case["n"], case["c"]
+    if op == "q8_rows":
+        return {"bytes": n * c * e + 2 * _q8_bytes(n, c) + 2 * n * c, "flops": 2 * n * c}
+    if op == "norm_fwd":
+        moved = n * c * e * (1 + 2 * case["res"] + (case["out"] != "8bit")) + 4 * n + c * e
+        # in 8 bits: written, and read back into values
+        return {"bytes": moved + (2 * _q8_bytes(n, c) + 2 * n * c if case["out"] != "rows" else 0), "flops": 5 * n * c}
+    saved = n * c * e if case["saved"] == "rows" else _q8_bytes(n, c)
+    return {"bytes": saved + n * c * e * (2 + case["dh"]) + 4 * n + c * e + 4 * c, "flops": 10 * n * c}
+
+
+# ----------------------------------------------------------------------------- in 64 bits
+def _exact_q8(v):
+    """The values that 8-bit rows of v (64 bits, finite) stand for, by the arithmetic of the format: a sign, 4 exponent
+    bits, 3 fraction bits, ties to even, steps of 2^-9 below 2^-6."""
+    n, c = v.shape
+    pad = -c % GROUP
+    w = torch.nn.functional.pad(v, (0, pad)).view(n, -1, GROUP)
+    top = w.abs().amax(2, keepdim=True)
+    _, k = torch.frexp(top / 448.0)                    # top / 448 = m 2^k, 1/2 <= m < 1
+    exact_power = torch.ldexp(torch.full_like(top, 448.0), k - 1) == top
+    k = torch.where(top > 0, torch.where(exact_power, k - 1, k), -126).clamp(min=-126)
+    u = torch.ldexp(w, -k)
+    _, f = torch.frexp(u)                              # |u| in [2^(f-1), 2^f)
+    step = (f - 1).clamp(min=-6) - 3
+    u = torch.ldexp(torch.round(torch.ldexp(u, -step)), step)
+    return torch.ldexp(u, k).reshape(n, -1)[:, :c]
+
+
+def _exact_values(q, e):
+    """The values of given 8-bit rows, from their bits."""
+    b = q.view(torch.uint8).long()
+    mag, ex = b & 7, (b >> 3) & 15
+    v = torch.where(ex > 0, torch.ldexp((8 + mag).double(), ex - 10), torch.ldexp(mag.double(), torch.full_like(ex, -9)))
+    v = torch.where(b >= 128, -v, v)
+    group = torch.arange(q.shape[1], device=q.device) // GROUP
+    return torch.ldexp(v, e.long()[:, group] - 127)
+
+
+def exact(case, seed):
+    global own
+    was, own = own, False  # the plain inputs: no handles of the framework
+    try:
+        s = prepare(case, seed)
+    finally:
+        own = was
+    op = case["op"]
+    if op == "embed_fwd":
+        ids = s["ids"].long()
+        table = torch.cat([s["table"], s["table"].new_zeros(1, case["c"])])  # the last row, -1, is the empty one
+        return torch.index_select(table, 0, ids % (case["vocab"] + 1)).double() * s["scale"]
+    if op == "embed_wgrad":
+        out = torch.zeros(case["vocab"] + 1, case["c"], device="cuda", dtype=torch.float64)
+        at = (s["ids"].long() % (case["vocab"] + 1))[:, None].expand(-1, case["c"])
+        out.scatter_add_(0, at, s["dy"].double() * s["scale"])
+        return out[:-1]
+    if op == "norm_fwd":
+        h = s["x"].double() if s["res"] is None else s["x"].double() + s["res"].double()
+        root = torch.sqrt(torch.linalg.vector_norm(h, dim=1) ** 2 / case["c"] + EPS)
+        y = h / root[:, None] * s["w"].double()
+        out = {"rstd": 1 / root}
+        if case["res"]:
+            out["h"] = h
+        if case["out"] != "8bit":
+            out["y"] = y
+        if case["out"] != "rows":
+            out["y8"] = _exact_q8(y)
+        return out
+    if op == "norm_bwd":
+        h = s["h"].double() if case["saved"] == "rows" else _exact_values(*s["h"])
+        r, dy, w = s["rstd"].double()[:, None], s["dy"].double(), s["w"].double()
+        along = torch.einsum("nc,c,nc->n", dy, w, h)[:, None]
+        dx = r * dy * w - r ** 3 / case["c"] * along * h
+        if s["dh"] is not None:
+            dx += s["dh"].double()
+        return {"dx": dx, "dw": torch.einsum("nc,nc,n->c", dy, h, r[:, 0])}
+    if op == "q8_rows":
+        return _exact_q8(s["x"].double())
+    x, dy = _exact_values(*s["xq"]), s["dy"].double()
+    return torch.stack([torch.einsum("pi,po->io", x[i], dy[j]) for i, j in s["pairs"]])
