@@ -78,8 +78,10 @@ def draw(rng):
             cin, cout = _channels(rng, 8, 64), _channels(rng, 8, 64)
             n = _log(rng, 100, 60000)
         batch = rng.choice([1, 2, 4])
-        grid = max(8, int((n / batch) ** (1 / 3) * rng.uniform(2.0, 6.0)))
-        return {"op": op, "n": n, "cin": cin, "cout": cout, "dtype": dtype, "batch": batch, "grid": grid}
+        grid = max(8, int((n / batch) ** (1 / 3) * rng.uniform(2.0, 8.0)))
+        case = {"op": op, "n": n, "cin": cin, "cout": cout, "dtype": dtype, "batch": batch, "grid": grid}
+        case["n"] = int(n * min(1.0, _pair_count(listed()[-1]) / _pair_count(case)))
+        return case
     c = _channels(rng, 8, 16384)
     n = _log(rng, 1, min(500000, (1 << 25) // c))
     if op == "q8_rows":
@@ -271,6 +273,14 @@ def run(state):
 
 
 # ----------------------------------------------------------------------------- work
+def _pair_count(case):
+    """About how many pairs a 3^3 submanifold layer's map has: the centre of every row, a third of a neighbour as scans
+    have them, and what the grid's density gives."""
+    n, grid = case["n"], case["grid"]
+    dense = n / (case["batch"] * grid * grid * (41 if grid > 100 else grid))
+    return int(n * min(27.0, 1.33 + 26 * dense))
+
+
 def _q8_bytes(n, c):
     return n * c + n * -(-c // GROUP)
 
@@ -285,7 +295,7 @@ def work(case):
         return {"bytes": ids + n * c * e + vocab * c * 4, "flops": n * c}
     if op == "q8_wgrad":
         n, cin, cout = case["n"], case["cin"], case["cout"]
-        pairs = int(1.35 * n)  # the centre of every row, and a third of a neighbour
+        pairs = _pair_count(case)
         return {"bytes": _q8_bytes(n, cin) + n * cout * e + 8 * pairs + 4 * 27 * cin * cout, "flops": 2 * pairs * cin * cout}
     n, c = case["n"], case["c"]
     if op == "q8_rows":
