@@ -74,7 +74,8 @@ typedef enum {
     LAT_ERR_CUDA = 64,        /* a CUDA runtime call failed (host)                      */
     LAT_ERR_WORKSPACE = 128,  /* ws_bytes smaller than the *_ws_bytes query (host)      */
     LAT_ERR_BAD_MAP = 256,    /* a kernel map holds a row index outside [0, n_in) (device) */
-    LAT_ERR_TIMEOUT = 512     /* a bounded in-kernel wait gave up; the kernel drained and exited */
+    LAT_ERR_TIMEOUT = 512,    /* a bounded in-kernel wait gave up; the kernel drained and exited */
+    LAT_ERR_BAD_ID = 1024     /* a token id is outside [0, vocab) and not the padding id (device) */
 } lat_status;
 
 typedef enum { LAT_F32 = 0, LAT_F16 = 1, LAT_BF16 = 2 } lat_dtype;
@@ -381,6 +382,95 @@ lat_status lat_sparse_pool(const void *x, int32_t c, const lat_kmap *map, int32_
 lat_status lat_to_dense(const int32_t *coords, int64_t n, const void *feats, int32_t c, lat_dtype dtype,
                         const int32_t *origin, const int32_t *shape, int32_t batch, void *out,
                         int32_t *d_status, lat_stream stream);
+
+/* ------------------------------------------- embedding of token rows ------
+ * Feature rows from categorical codes (a voxel's class, a token's id), in
+ * front of the first convolution:
+ *   y[i] = scale * table[ids[i]]
+ * and the table's gradient, for every t in [0, vocab):
+ *   dtable[t] = scale * sum over { i : ids[i] == t } of dy[i]
+ *   ids     device int32 (id_bytes 4) or int64 (id_bytes 8) [n].  A row whose
+ *           id is pad_id (any value, -1 for instance) has no token: its y is
+ *           0 and its dy counts nowhere.  Another id outside [0, vocab) does
+ *           the same and sets LAT_ERR_BAD_ID at d_status (may be NULL).
+ *   table   device [vocab][c], y and dy device [n][c], of dtype, 16-byte
+ *           aligned, without overlap; c a multiple of 8 in [8, 16384];
+ *           n < 2^31, 1 <= vocab < 2^31 - 1.
+ *   dtable  device fp32 [vocab][c], 16-byte aligned; every row is written
+ *           (0 for a token without rows).
+ * Arithmetic is fp32, one rounding to dtype.  The gradient sorts the rows by
+ * token and adds each token's rows in parts whose sizes and order depend on
+ * the arguments' sizes alone (no atomics on sums): its bits are the same on
+ * every call.  Workspace as for the other ops (16-byte aligned); lookup
+ * takes none.  Asynchronous on `stream`; allocates nothing. */
+lat_status lat_embed_fwd(const void *ids, int32_t id_bytes, int64_t n, const void *table, int64_t vocab,
+                         int32_t c, float scale, int64_t pad_id, void *y, lat_dtype dtype,
+                         int32_t *d_status, lat_stream stream);
+size_t lat_embed_wgrad_ws_bytes(int64_t n, int64_t vocab, int32_t c);
+lat_status lat_embed_wgrad(const void *ids, int32_t id_bytes, int64_t n, const void *dy, int64_t vocab,
+                           int32_t c, float scale, int64_t pad_id, float *dtable, lat_dtype dtype,
+                           void *ws, size_t ws_bytes, int32_t *d_status, lat_stream stream);
+
+/* ------------------------------------------------------ rows in 8 bits ----
+ * Activation checkpoints: what a backward pass needs of the forward pass's
+ * rows, kept in 8 bits.  For rows of c channels a buffer q of e4m3 values
+ * [n][c] and a buffer of scale bytes [n][ceil(c/32)]: channels 32g..32g+31
+ * of a row share the scale 2^(E-127), E their byte, the smallest E >= 1 with
+ * max |v| <= 448 * 2^(E-127) over their finite values, and
+ *   q = e4m3(v / scale), rounded to nearest even (exact division).
+ * So a value is off by at most 2^-4 of itself (2^-10 of the scale below
+ * 2^-6 of it).  Infinities and NaN are stored as NaN.  lat_q8_unpack writes
+ * q * scale in dtype: exact in fp32 and bf16 (subnormals aside); in fp16
+ * rounded to nearest and held at +-65504.
+ *   x   device [n][c] of dtype; q device [n][c] bytes; both 16-byte
+ *       aligned, no overlap; c a multiple of 8 in [8, 16384]; n < 2^31.
+ * Readers of 8-bit rows: lat_q8_unpack, lat_sconv_wgrad_q8 (the rows that a
+ * convolution was given), lat_rms_norm_bwd (the rows that a norm was given).
+ * Asynchronous on `stream`; allocates nothing. */
+#define LAT_Q8_GROUP 32
+lat_status lat_q8_pack(const void *x, int64_t n, int32_t c, void *q, void *scale, lat_dtype dtype,
+                       lat_stream stream);
+lat_status lat_q8_unpack(const void *q, const void *scale, int64_t n, int32_t c, void *x, lat_dtype dtype,
+                         lat_stream stream);
+
+/* lat_sconv_wgrad with x (map->n_in, cin) in 8 bits: dW[k] = sum over pairs
+ * (i, j) of offset k of (q * scale)[i]^T dy[j], fp32.  dtype is dy's.
+ * Limits, determinism and errors as for lat_sconv_wgrad. */
+size_t lat_sconv_wgrad_q8_ws_bytes(int32_t cin, int32_t cout, const lat_kmap *map, lat_dtype dtype);
+lat_status lat_sconv_wgrad_q8(const void *q, const void *scale, int32_t cin, const void *dy, int32_t cout,
+                              const lat_kmap *map, float *dw, lat_dtype dtype, void *ws, size_t ws_bytes,
+                              int32_t *d_status, lat_stream stream);
+
+/* ------------------------------------------------------------ RMS norm ----
+ * Root-mean-square norm of feature rows with the residual's addition:
+ *   h = x + res      rstd = (mean_c h^2 + eps)^(-1/2)      y = h * rstd * w
+ * x, res, h, y device [n][c] and w device [c], of dtype; rstd device fp32
+ * [n].  res NULL: h = x.  w NULL: all ones.  Every output may be NULL: h
+ * (the residual stream for the next layer), y, y in 8 bits (y8 with
+ * y8_scale, lat_q8_pack's format), h in 8 bits (h8 with h8_scale: what
+ * lat_rms_norm_bwd needs), rstd.  Each output is rounded once, from fp32: y
+ * and the 8-bit rows do not come from a rounded h.  h may be x or res
+ * itself; no other overlap.  eps > 0.  The mean of the squares must be
+ * finite in fp32. */
+lat_status lat_rms_norm_fwd(const void *x, const void *res, const void *w, int64_t n, int32_t c, float eps,
+                            void *h, void *y, void *y8, void *y8_scale, void *h8, void *h8_scale,
+                            float *rstd, lat_dtype dtype, lat_stream stream);
+
+/* Backward pass: with g = dy * w and xh = h * rstd
+ *   dx = rstd * (g - xh * mean_c(g * xh)) + dh      (the gradient of x and of res)
+ *   dw = sum over rows of dy * xh                   (fp32 [c]; NULL: not wanted)
+ * h: the forward pass's h in dtype, or NULL and h8 / h8_scale its 8-bit rows.
+ * dh: the gradient that reaches h past the norm, NULL for none.  dx may be
+ * dy or dh itself; no other overlap.  The sums of dw run in a fixed order
+ * over parts that depend on n and c alone.  Workspace (16-byte aligned) only
+ * for dw.  Both passes: 16-byte aligned rows, c a multiple of 8 in
+ * [8, 16384], n < 2^31, fp32 arithmetic; asynchronous on `stream`; they
+ * allocate nothing. */
+size_t lat_rms_norm_bwd_ws_bytes(int64_t n, int32_t c);
+lat_status lat_rms_norm_bwd(const void *dy, const void *dh, const void *h, const void *h8,
+                            const void *h8_scale, const float *rstd, const void *w, int64_t n, int32_t c,
+                            void *dx, float *dw, lat_dtype dtype, void *ws, size_t ws_bytes,
+                            lat_stream stream);
 
 /* ---------------------------------------------------------------- misc --- */
 

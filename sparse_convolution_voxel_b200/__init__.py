@@ -10,8 +10,21 @@ Typical SubmConv3d forward (Torch Lattice docs, "Convolution mapping"):
     table = hash_table(coords)                       # lat_hash_build
     kmap = kernel_map(table, coords, coords, subm_geom(3))   # lat_kmap_query
     y = conv_fwd(x, w, kmap)                         # lat_sconv_fwd
+
+A training step that keeps 8-bit checkpoints instead of rows:
+
+    x = embed_fwd(ids, table, scale)                 # lat_embed_fwd
+    f = rms_norm_fwd(x, g, res, q8=True, q8_h=True)  # lat_rms_norm_fwd
+    y = conv_fwd(f.y, w, kmap)                       # f.y is not needed any more after this
+    ...
+    dw = conv_wgrad_q8(f.y8, dy, kmap)               # lat_sconv_wgrad_q8
+    dn = conv_dgrad(dy, w, kmap, True)
+    dx, dg = rms_norm_bwd(dn, f.h8, f.rstd, g, dh)   # lat_rms_norm_bwd
+    dt = embed_wgrad(ids, dx, len(table), scale)     # lat_embed_wgrad
 """
 from __future__ import annotations
+
+from collections import namedtuple
 
 import torch
 
@@ -21,6 +34,8 @@ from ._lib import (  # noqa: F401  (re-exported C entry points and constants)
     lat_upsample_coords, lat_upsample_ws_bytes,
     lat_hash_build, lat_hash_bytes, lat_kmap, lat_kmap_from_parent, lat_kmap_from_parent_ws_bytes, lat_kmap_query,
     lat_kmap_ws_bytes, lat_sconv_dgrad, lat_sconv_fwd, lat_sparse_pool, lat_to_dense,
+    LAT_Q8_GROUP, lat_embed_fwd, lat_embed_wgrad, lat_embed_wgrad_ws_bytes, lat_q8_pack, lat_q8_unpack,
+    lat_rms_norm_bwd, lat_rms_norm_bwd_ws_bytes, lat_rms_norm_fwd, lat_sconv_wgrad_q8, lat_sconv_wgrad_q8_ws_bytes,
     lat_sconv_wgrad, lat_sconv_wgrad_static, lat_sconv_ws_bytes, lat_set_wait_limit_ns, lat_status_fetch,
     lat_status_string, lat_version, load, make_geom,
 )
@@ -28,6 +43,8 @@ from ._lib import (  # noqa: F401  (re-exported C entry points and constants)
 __all__ = [
     "KernelMap", "Workspace", "hash_table", "kernel_map", "downsample", "downsample_async", "PendingDownsample",
     "upsample", "maps_from_parent", "conv_fwd", "conv_dgrad", "conv_wgrad", "sparse_pool", "to_dense",
+    "embed_fwd", "embed_wgrad", "Q8Rows", "q8_pack", "q8_unpack", "conv_wgrad_q8", "RmsNorm", "rms_norm_fwd",
+    "rms_norm_bwd",
     "subm_geom", "strided_geom", "target_geom", "transposed_geom", "check_status", "new_status",
 ] + EXPORTS
 
@@ -259,3 +276,133 @@ def to_dense(coords, feats, origin, shape, batch: int, d_status=None, out=None, 
     grid = out if out is not None else torch.empty(size, dtype=feats.dtype, device=feats.device)
     lat_to_dense(coords, feats, origin, shape, batch, grid, d_status, stream)
     return grid
+
+
+class _on:
+    """Makes `stream` (a torch.cuda.Stream or a raw handle; None: leave it) the current stream, so that
+    the buffers a helper allocates belong to the stream that its kernels run on."""
+
+    def __init__(self, stream, device):
+        self.guard = None
+        if stream is not None:
+            if isinstance(stream, int):
+                stream = torch.cuda.ExternalStream(stream, device)
+            self.guard = torch.cuda.stream(stream)
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+
+def embed_fwd(ids, table, scale: float = 1.0, pad_id: int = -1, d_status=None, out=None, stream=None):
+    """scale * table[ids] (n, c); rows whose id is pad_id are 0.  ids int32 or int64 (n,)."""
+    with _on(stream, table.device):
+        y = out if out is not None else torch.empty((ids.shape[0], table.shape[1]), dtype=table.dtype,
+                                                    device=table.device)
+        lat_embed_fwd(ids, table, scale, pad_id, y, d_status, stream)
+    return y
+
+
+def embed_wgrad(ids, dy, vocab: int, scale: float = 1.0, pad_id: int = -1, ws: Workspace | None = None, d_status=None,
+                out=None, stream=None):
+    """The table's gradient (vocab, c) in fp32: scale * the sum of dy's rows of each token."""
+    with _on(stream, dy.device):
+        dt = out if out is not None else torch.empty((int(vocab), dy.shape[1]), dtype=torch.float32, device=dy.device)
+        if dt.shape[0] != vocab:
+            raise ValueError(f"out has {dt.shape[0]} rows, not {vocab}")
+        ws = ws or Workspace(dy.device)
+        lat_embed_wgrad(ids, dy, scale, pad_id, dt, ws.get(lat_embed_wgrad_ws_bytes(dy.shape[0], vocab, dy.shape[1])),
+                        d_status, stream)
+    return dt
+
+
+class Q8Rows:
+    """Feature rows in 8 bits: q float8_e4m3fn (n, c) and scale uint8 (n, ceil(c/32)), the scales'
+    exponent bytes (see include/lattice.h, "rows in 8 bits")."""
+
+    __slots__ = ("q", "scale")
+
+    def __init__(self, q: torch.Tensor, scale: torch.Tensor):
+        self.q, self.scale = q, scale
+
+    @classmethod
+    def empty(cls, n: int, c: int, device="cuda") -> "Q8Rows":
+        return cls(torch.empty((n, c), dtype=torch.float8_e4m3fn, device=device),
+                   torch.empty((n, -(-c // LAT_Q8_GROUP)), dtype=torch.uint8, device=device))
+
+    @property
+    def shape(self):
+        return self.q.shape
+
+    @property
+    def nbytes(self) -> int:
+        return self.q.numel() + self.scale.numel()
+
+
+def q8_pack(x, out: Q8Rows | None = None, stream=None) -> Q8Rows:
+    """x (n, c) as 8-bit rows."""
+    with _on(stream, x.device):
+        r = out if out is not None else Q8Rows.empty(x.shape[0], x.shape[1], x.device)
+        lat_q8_pack(x, r.q, r.scale, stream)
+    return r
+
+
+def q8_unpack(rows: Q8Rows, dtype: torch.dtype = torch.bfloat16, out=None, stream=None):
+    """The values of 8-bit rows in dtype."""
+    with _on(stream, rows.q.device):
+        x = out if out is not None else torch.empty(rows.q.shape, dtype=dtype, device=rows.q.device)
+        lat_q8_unpack(rows.q, rows.scale, x, stream)
+    return x
+
+
+def conv_wgrad_q8(x: Q8Rows, dy, kmap: KernelMap, ws: Workspace | None = None, d_status=None, out=None, stream=None):
+    """conv_wgrad with the convolution's input rows in 8 bits."""
+    cin, cout = x.q.shape[1], dy.shape[1]
+    with _on(stream, dy.device):
+        dw = out if out is not None else torch.empty((kmap.k3, cin, cout), dtype=torch.float32, device=dy.device)
+        ws = ws or Workspace(dy.device)
+        lat_sconv_wgrad_q8(x.q, x.scale, dy, kmap.c, dw,
+                           ws.get(lat_sconv_wgrad_q8_ws_bytes(cin, cout, kmap.c, dy.dtype)), d_status, stream)
+    return dw
+
+
+RmsNorm = namedtuple("RmsNorm", "y h rstd y8 h8")
+
+
+def rms_norm_fwd(x, w=None, res=None, eps: float = 1e-6, rows: bool = True, q8: bool = False, q8_h: bool = False,
+                 h_out=None, stream=None) -> RmsNorm:
+    """RMS norm of h = x + res over the channels: RmsNorm(y, h, rstd, y8, h8).
+
+    y is None without ``rows``, y8 (y in 8 bits) without ``q8`` and h8 (h in 8 bits, for rms_norm_bwd)
+    without ``q8_h``.  h is x itself without ``res``; ``h_out`` (x or res, to add in place, or another
+    tensor) receives h."""
+    n, c = x.shape
+    with _on(stream, x.device):
+        h = h_out if h_out is not None else torch.empty_like(x) if res is not None else None
+        y = torch.empty_like(x) if rows else None
+        rstd = torch.empty(n, dtype=torch.float32, device=x.device)
+        y8 = Q8Rows.empty(n, c, x.device) if q8 else None
+        h8 = Q8Rows.empty(n, c, x.device) if q8_h else None
+        lat_rms_norm_fwd(x, res, w, eps, h, y, y8.q if q8 else None, y8.scale if q8 else None, h8.q if q8_h else None,
+                         h8.scale if q8_h else None, rstd, stream)
+    return RmsNorm(y, x if h is None else h, rstd, y8, h8)
+
+
+def rms_norm_bwd(dy, h, rstd, w=None, dh=None, want_dw: bool = True, ws: Workspace | None = None, out=None, stream=None):
+    """(dx, dw) of rms_norm_fwd from h (rows, or their Q8Rows) and rstd: dx, the gradient of x and of res
+    alike, with dh (the gradient that reaches h past the norm) added; dw in fp32, None without ``want_dw``."""
+    with _on(stream, dy.device):
+        dx = out if out is not None else torch.empty_like(dy)
+        dw = torch.empty(dy.shape[1], dtype=torch.float32, device=dy.device) if want_dw else None
+        buf = None
+        if want_dw:
+            ws = ws or Workspace(dy.device)
+            buf = ws.get(lat_rms_norm_bwd_ws_bytes(dy.shape[0], dy.shape[1]))
+        q = isinstance(h, Q8Rows)
+        lat_rms_norm_bwd(dy, dh, None if q else h, h.q if q else None, h.scale if q else None, rstd, w, dx, dw, buf,
+                         stream)
+    return dx, dw

@@ -22,11 +22,12 @@ LAT_SUBM, LAT_STRIDED, LAT_TRANSPOSED = 0, 1, 2
 LAT_OP_FWD, LAT_OP_DGRAD, LAT_OP_WGRAD = 0, 1, 2
 LAT_TILE_ROWS = 128
 LAT_POOL_MAX, LAT_POOL_AVG = 0, 1
+LAT_Q8_GROUP = 32
 
 STATUS_BITS = {
     1: "LAT_ERR_ARG", 2: "LAT_ERR_COORD_RANGE", 4: "LAT_ERR_DUPLICATE", 8: "LAT_ERR_TABLE_FULL",
     16: "LAT_ERR_CAPACITY", 32: "LAT_ERR_UNSUPPORTED", 64: "LAT_ERR_CUDA", 128: "LAT_ERR_WORKSPACE",
-    256: "LAT_ERR_BAD_MAP", 512: "LAT_ERR_TIMEOUT",
+    256: "LAT_ERR_BAD_MAP", 512: "LAT_ERR_TIMEOUT", 1024: "LAT_ERR_BAD_ID",
 }
 
 # every symbol include/lattice.h declares
@@ -37,6 +38,9 @@ EXPORTS = [
     "lat_kmap_from_parent",
     "lat_sconv_ws_bytes", "lat_sconv_fwd",
     "lat_sconv_dgrad", "lat_sconv_wgrad", "lat_sconv_wgrad_static", "lat_sparse_pool", "lat_to_dense",
+    "lat_embed_fwd", "lat_embed_wgrad_ws_bytes", "lat_embed_wgrad", "lat_q8_pack", "lat_q8_unpack",
+    "lat_sconv_wgrad_q8_ws_bytes", "lat_sconv_wgrad_q8", "lat_rms_norm_fwd", "lat_rms_norm_bwd_ws_bytes",
+    "lat_rms_norm_bwd",
     "lat_status_fetch", "lat_status_string", "lat_version", "lat_set_wait_limit_ns",
 ]
 
@@ -73,6 +77,7 @@ def load() -> ctypes.CDLL:
         raise ImportError(f"liblattice.so not built ({LIB_PATH}); run sparse_convolution_voxel_b200/build.py")
     lib = ctypes.CDLL(LIB_PATH)
     P, I32, I64, SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
+    F = ctypes.c_float
     G, K = ctypes.POINTER(lat_geom), ctypes.POINTER(lat_kmap)
     sig = {
         "lat_hash_bytes": (SZ, [I64, ctypes.c_float]),
@@ -93,6 +98,16 @@ def load() -> ctypes.CDLL:
         "lat_sconv_wgrad_static": (I32, [P, I32, P, I32, K, P, I32, P, P]),
         "lat_sparse_pool": (I32, [P, I32, K, I32, P, I32, P, P]),
         "lat_to_dense": (I32, [P, I64, P, I32, I32, ctypes.POINTER(I32), ctypes.POINTER(I32), I32, P, P, P]),
+        "lat_embed_fwd": (I32, [P, I32, I64, P, I64, I32, F, I64, P, I32, P, P]),
+        "lat_embed_wgrad_ws_bytes": (SZ, [I64, I64, I32]),
+        "lat_embed_wgrad": (I32, [P, I32, I64, P, I64, I32, F, I64, P, I32, P, SZ, P, P]),
+        "lat_q8_pack": (I32, [P, I64, I32, P, P, I32, P]),
+        "lat_q8_unpack": (I32, [P, P, I64, I32, P, I32, P]),
+        "lat_sconv_wgrad_q8_ws_bytes": (SZ, [I32, I32, K, I32]),
+        "lat_sconv_wgrad_q8": (I32, [P, P, I32, P, I32, K, P, I32, P, SZ, P, P]),
+        "lat_rms_norm_fwd": (I32, [P, P, P, I64, I32, F, P, P, P, P, P, P, P, I32, P]),
+        "lat_rms_norm_bwd_ws_bytes": (SZ, [I64, I32]),
+        "lat_rms_norm_bwd": (I32, [P, P, P, P, P, P, P, I64, I32, P, P, I32, P, SZ, P]),
         "lat_status_fetch": (I32, [P, P]),
         "lat_status_string": (ctypes.c_char_p, [I32]),
         "lat_version": (I32, []),
@@ -285,6 +300,155 @@ def lat_to_dense(coords, feats, origin, shape, batch: int, out, d_status=None, s
     rc = load().lat_to_dense(_ptr(coords), coords.shape[0], _ptr(feats), feats.shape[1], dtype_code(feats.dtype), o,
                              sh, int(batch), _ptr(out), _ptr(d_status), _stream(stream))
     _check(rc, "lat_to_dense")
+
+
+def _rows(x, what: str, n=None, c=None, dtype=None, like=None):
+    """Checks one argument of a row-wise entry point: 2-D, of shape (n, c), of dtype, on like's device."""
+    if x.dim() != 2 or (n is not None and x.shape[0] != n) or (c is not None and x.shape[1] != c):
+        raise ValueError(f"{what} has shape {tuple(x.shape)}, not ({'n' if n is None else n}, {'c' if c is None else c})")
+    if x.dtype != dtype if dtype is not None else x.dtype not in _DTYPE_CODE:
+        raise ValueError(f"{what} has type {x.dtype}, not {dtype or 'float32, float16 or bfloat16'}")
+    _same_device(x, what, like)
+
+
+def _vector(x, what: str, n, dtype, like):
+    if x.dim() != 1 or x.shape[0] != n or x.dtype not in (dtype if isinstance(dtype, tuple) else (dtype,)):
+        raise ValueError(f"{what} is {x.dtype} {tuple(x.shape)}, not {dtype} ({n},)")
+    _same_device(x, what, like)
+
+
+def _same_device(x, what: str, like):
+    """All tensors of a call lie on one device, which is the current one (the launch goes to the current device's stream)."""
+    if x.is_cuda:
+        here = like.device.index if like is not None else (_cur_dev() if _cur_dev is not None else
+                                                            torch.cuda.current_device())
+        if x.device.index != here:
+            raise ValueError(f"{what} is on {x.device}, the call on cuda:{here}: use torch.cuda.device")
+
+
+def _scratch(ws, like):
+    """(pointer, bytes) of a workspace on like's device."""
+    if ws is not None:
+        _same_device(ws, "ws", like)
+    return _ws_args(ws)
+
+
+def _status_word(d_status, like):
+    if d_status is not None:
+        _vector(d_status, "d_status", 1, torch.int32, like)
+
+
+def _q8_rows(q, scale, what: str, like, n=None, c=None):
+    _rows(q, what, n, c, torch.float8_e4m3fn, like)
+    _rows(scale, what + " scale", q.shape[0], -(-q.shape[1] // LAT_Q8_GROUP), torch.uint8, like if like is not None else q)
+
+
+def lat_embed_fwd(ids, table, scale: float, pad_id: int, y, d_status=None, stream=None):
+    _rows(table, "table")
+    _vector(ids, "ids", ids.shape[0] if ids.dim() == 1 else -1, (torch.int32, torch.int64), table)
+    _rows(y, "y", ids.shape[0], table.shape[1], table.dtype, table)
+    _status_word(d_status, table)
+    rc = load().lat_embed_fwd(_ptr(ids), ids.element_size(), ids.shape[0], _ptr(table), table.shape[0], table.shape[1],
+                              float(scale), int(pad_id), _ptr(y), dtype_code(table.dtype), _ptr(d_status),
+                              _stream(stream))
+    _check(rc, "lat_embed_fwd")
+
+
+def lat_embed_wgrad_ws_bytes(n: int, vocab: int, c: int) -> int:
+    return int(load().lat_embed_wgrad_ws_bytes(int(n), int(vocab), int(c)))
+
+
+def lat_embed_wgrad(ids, dy, scale: float, pad_id: int, dtable, ws=None, d_status=None, stream=None):
+    _rows(dy, "dy")
+    _vector(ids, "ids", dy.shape[0], (torch.int32, torch.int64), dy)
+    _rows(dtable, "dtable", None, dy.shape[1], torch.float32, dy)
+    _status_word(d_status, dy)
+    p, n = _scratch(ws, dy)
+    rc = load().lat_embed_wgrad(_ptr(ids), ids.element_size(), ids.shape[0], _ptr(dy), dtable.shape[0], dy.shape[1],
+                                float(scale), int(pad_id), _ptr(dtable), dtype_code(dy.dtype), p, n, _ptr(d_status),
+                                _stream(stream))
+    _check(rc, "lat_embed_wgrad")
+
+
+def lat_q8_pack(x, q, scale, stream=None):
+    _rows(x, "x")
+    _q8_rows(q, scale, "q", x, *x.shape)
+    rc = load().lat_q8_pack(_ptr(x), x.shape[0], x.shape[1], _ptr(q), _ptr(scale), dtype_code(x.dtype),
+                            _stream(stream))
+    _check(rc, "lat_q8_pack")
+
+
+def lat_q8_unpack(q, scale, x, stream=None):
+    _rows(x, "x")
+    _q8_rows(q, scale, "q", x, *x.shape)
+    rc = load().lat_q8_unpack(_ptr(q), _ptr(scale), x.shape[0], x.shape[1], _ptr(x), dtype_code(x.dtype),
+                              _stream(stream))
+    _check(rc, "lat_q8_unpack")
+
+
+def lat_sconv_wgrad_q8_ws_bytes(cin: int, cout: int, kmap: lat_kmap, dtype: torch.dtype) -> int:
+    return int(load().lat_sconv_wgrad_q8_ws_bytes(int(cin), int(cout), ctypes.byref(kmap), dtype_code(dtype)))
+
+
+def lat_sconv_wgrad_q8(q, scale, dy, kmap: lat_kmap, dw, ws=None, d_status=None, stream=None):
+    _rows(dy, "dy", kmap.n_out)
+    _q8_rows(q, scale, "q", dy, kmap.n_in)
+    cin, cout = q.shape[1], dy.shape[1]
+    if dw.dtype != torch.float32 or tuple(dw.shape) != (kmap.k3, cin, cout):
+        raise ValueError(f"dw is {dw.dtype} {tuple(dw.shape)}, not float32 {(kmap.k3, cin, cout)}")
+    _same_device(dw, "dw", dy)
+    _status_word(d_status, dy)
+    p, n = _scratch(ws, dy)
+    rc = load().lat_sconv_wgrad_q8(_ptr(q), _ptr(scale), cin, _ptr(dy), cout, ctypes.byref(kmap), _ptr(dw),
+                                   dtype_code(dy.dtype), p, n, _ptr(d_status), _stream(stream))
+    _check(rc, "lat_sconv_wgrad_q8")
+
+
+def lat_rms_norm_fwd(x, res, w, eps: float, h=None, y=None, y8=None, y8_scale=None, h8=None, h8_scale=None, rstd=None,
+                     stream=None):
+    _rows(x, "x")
+    n, c = x.shape
+    for t, what in ((res, "res"), (h, "h"), (y, "y")):
+        if t is not None:
+            _rows(t, what, n, c, x.dtype, x)
+    for q, s, what in ((y8, y8_scale, "y8"), (h8, h8_scale, "h8")):
+        if (q is None) != (s is None):
+            raise ValueError(f"{what} needs its values and its scales")
+        if q is not None:
+            _q8_rows(q, s, what, x, n, c)
+    if w is not None:
+        _vector(w, "w", c, x.dtype, x)
+    if rstd is not None:
+        _vector(rstd, "rstd", n, torch.float32, x)
+    rc = load().lat_rms_norm_fwd(_ptr(x), _ptr(res), _ptr(w), n, c, float(eps), _ptr(h), _ptr(y), _ptr(y8),
+                                 _ptr(y8_scale), _ptr(h8), _ptr(h8_scale), _ptr(rstd), dtype_code(x.dtype),
+                                 _stream(stream))
+    _check(rc, "lat_rms_norm_fwd")
+
+
+def lat_rms_norm_bwd_ws_bytes(n: int, c: int) -> int:
+    return int(load().lat_rms_norm_bwd_ws_bytes(int(n), int(c)))
+
+
+def lat_rms_norm_bwd(dy, dh, h, h8, h8_scale, rstd, w, dx, dw=None, ws=None, stream=None):
+    _rows(dy, "dy")
+    n, c = dy.shape
+    if (h is None) == (h8 is None) or (h8 is None) != (h8_scale is None):
+        raise ValueError("rms_norm_bwd takes h, or its 8-bit values and their scales")
+    for t, what in ((dh, "dh"), (h, "h"), (dx, "dx")):
+        if t is not None:
+            _rows(t, what, n, c, dy.dtype, dy)
+    if h8 is not None:
+        _q8_rows(h8, h8_scale, "h8", dy, n, c)
+    _vector(rstd, "rstd", n, torch.float32, dy)
+    if w is not None:
+        _vector(w, "w", c, dy.dtype, dy)
+    if dw is not None:
+        _vector(dw, "dw", c, torch.float32, dy)
+    p, nb = _scratch(ws, dy)
+    rc = load().lat_rms_norm_bwd(_ptr(dy), _ptr(dh), _ptr(h), _ptr(h8), _ptr(h8_scale), _ptr(rstd), _ptr(w), n, c,
+                                 _ptr(dx), _ptr(dw), dtype_code(dy.dtype), p, nb, _stream(stream))
+    _check(rc, "lat_rms_norm_bwd")
 
 
 def lat_status_fetch(d_status: torch.Tensor, stream=None) -> int:

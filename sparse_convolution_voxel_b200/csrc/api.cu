@@ -101,6 +101,35 @@ extern "C" lat_status lat_sconv_wgrad(const void *x, int32_t cin, const void *dy
     });
 }
 
+// The rows in dy's type, in front of lat_sconv_wgrad's own workspace.
+static size_t q8_rows_bytes(int32_t cin, const lat_kmap *map, lat_dtype dtype) {
+    return lat::align_up(size_t(map->n_in) * size_t(cin) * (dtype == LAT_F32 ? 4 : 2), 256);
+}
+
+extern "C" size_t lat_sconv_wgrad_q8_ws_bytes(int32_t cin, int32_t cout, const lat_kmap *map, lat_dtype dtype) {
+    if (!lat::map_ok(map) || !lat::chan_ok(cin, dtype) || !lat::chan_ok(cout, dtype)) return 0;
+    return q8_rows_bytes(cin, map, dtype) + lat_sconv_ws_bytes(LAT_OP_WGRAD, cin, cout, map, dtype);
+}
+
+extern "C" lat_status lat_sconv_wgrad_q8(const void *q, const void *scale, int32_t cin, const void *dy, int32_t cout,
+                                         const lat_kmap *map, float *dw, lat_dtype dtype, void *ws, size_t ws_bytes,
+                                         int32_t *d_status, lat_stream stream) {
+    using namespace lat;
+    if (!map_ok(map) || !chan_ok(cin, dtype) || !chan_ok(cout, dtype) || !dw || !map->pair_off) return LAT_ERR_ARG;
+    if (dtype != LAT_F32 && dtype != LAT_F16 && dtype != LAT_BF16) return LAT_ERR_ARG;
+    if (map->n_in > 0 && (!q || !scale)) return LAT_ERR_ARG;
+    if (!aligned16(q) || !aligned16(dy) || !aligned16(dw)) return LAT_ERR_ARG;
+    if (map->pair_capacity > 0 && (!map->pair_in || !map->pair_out)) return LAT_ERR_ARG;
+    if (!ws || !aligned16(ws) || ws_bytes < lat_sconv_wgrad_q8_ws_bytes(cin, cout, map, dtype))
+        return LAT_ERR_WORKSPACE;
+    const lat_status st =
+        launch_q8_unpack(q, scale, map->n_in, cin, ws, dtype, reinterpret_cast<cudaStream_t>(stream));
+    if (st != LAT_OK) return st;
+    const size_t used = q8_rows_bytes(cin, map, dtype);
+    return lat_sconv_wgrad(ws, cin, dy, cout, map, dw, dtype, static_cast<char *>(ws) + used, ws_bytes - used, d_status,
+                           stream);
+}
+
 extern "C" int32_t lat_status_fetch(const int32_t *d_status, lat_stream stream) {
     if (!d_status) return LAT_ERR_ARG;
     int32_t v = 0;
@@ -122,6 +151,7 @@ extern "C" const char *lat_status_string(int32_t status) {
     if (status & LAT_ERR_WORKSPACE) return "workspace too small";
     if (status & LAT_ERR_BAD_MAP) return "kernel map row index out of range";
     if (status & LAT_ERR_TIMEOUT) return "bounded in-kernel wait timed out";
+    if (status & LAT_ERR_BAD_ID) return "token id out of range";
     return "unknown status";
 }
 

@@ -1,0 +1,140 @@
+// Feature rows in 8-channel slices: the loads, stores and the 8-bit form shared by the
+// row-wise kernels (norm.cu, embed.cu, q8.cu).
+#pragma once
+
+#include <cuda_fp8.h>
+#include <float.h>
+
+#include "common.cuh"
+
+namespace lat {
+namespace rows {
+
+// 8 consecutive channels of one row: 16 bytes (fp16 / bf16) or 32 (fp32).
+template <typename T> struct Slice8 {
+    uint4 v[sizeof(T) / 2];
+};
+
+// A plain load: several entry points may write a row over the one they read.
+template <typename T>
+__device__ __forceinline__ Slice8<T> ld(const T *p) {
+    Slice8<T> s;
+#pragma unroll
+    for (int h = 0; h < int(sizeof(T) / 2); ++h) s.v[h] = reinterpret_cast<const uint4 *>(p)[h];
+    return s;
+}
+template <typename T>
+__device__ __forceinline__ Slice8<T> zero_slice() {
+    Slice8<T> s;
+#pragma unroll
+    for (int h = 0; h < int(sizeof(T) / 2); ++h) s.v[h] = make_uint4(0u, 0u, 0u, 0u);
+    return s;
+}
+template <typename T>
+__device__ __forceinline__ void to_f(const Slice8<T> &s, float (&v)[8]) {
+    const T *e = reinterpret_cast<const T *>(s.v);
+#pragma unroll
+    for (int c = 0; c < 8; ++c) v[c] = Elem<T>::to_f(e[c]);
+}
+template <typename T>
+__device__ __forceinline__ void st(T *p, const float (&v)[8]) {
+    Slice8<T> s;
+    T *e = reinterpret_cast<T *>(s.v);
+#pragma unroll
+    for (int c = 0; c < 8; ++c) e[c] = Elem<T>::from_f(v[c]);
+#pragma unroll
+    for (int h = 0; h < int(sizeof(T) / 2); ++h) reinterpret_cast<uint4 *>(p)[h] = s.v[h];
+}
+
+// ------------------------------------------------------------------- 8-bit rows
+// A group of 32 channels of one row shares the scale 2^(E - 127), E >= 1 the smallest
+// exponent byte with amax <= 448 * scale (448: the largest e4m3 value), amax over the
+// finite values; a value is stored as e4m3(v / scale), rounded to nearest even.  The
+// division by a power of two is exact, so the one rounding is e4m3's (at most 2^-4 of
+// the value, or 2^-10 scale below 2^-6 scale), and scale * e4m3 has 4 significant bits:
+// bf16 holds it exactly.
+constexpr int kQ8Group = 32;
+
+__host__ __device__ __forceinline__ int q8_groups(int c) { return (c + kQ8Group - 1) / kQ8Group; }
+
+// amax = m 2^x with 1 <= m < 2: the scale is 2^(x - 8) while m <= 1.75, else 2^(x - 7).
+// Adding 0x1FFFFF carries into the exponent exactly for mantissas above 1.75.
+__device__ __forceinline__ int q8_exponent(float amax) {
+    return max(1, int((__float_as_uint(amax) + 0x1FFFFFu) >> 23) - 8);
+}
+__device__ __forceinline__ float q8_scale(int e) { return __uint_as_float(uint32_t(e) << 23); }
+__device__ __forceinline__ float q8_inverse(int e) { return __uint_as_float(uint32_t(254 - e) << 23); }
+
+// Largest finite magnitude of 8 channels (0 if none is finite).
+__device__ __forceinline__ float finite_amax(const float (&v)[8]) {
+    float m = 0.f;
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+        const float a = fabsf(v[c]);
+        m = fmaxf(m, a <= FLT_MAX ? a : 0.f);
+    }
+    return m;
+}
+
+__device__ __forceinline__ uint32_t q8_pair(float a, float b) {
+    return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+}
+// 8 channels to e4m3; what is not finite becomes NaN (the format has no infinity).
+__device__ __forceinline__ uint2 q8_from_f(const float (&v)[8], int e) {
+    const float inv = q8_inverse(e);
+    float u[8];
+#pragma unroll
+    for (int c = 0; c < 8; ++c) u[c] = fabsf(v[c]) <= FLT_MAX ? v[c] * inv : __int_as_float(0x7FFFFFFF);
+    return make_uint2(q8_pair(u[0], u[1]) | (q8_pair(u[2], u[3]) << 16),
+                      q8_pair(u[4], u[5]) | (q8_pair(u[6], u[7]) << 16));
+}
+__device__ __forceinline__ void q8_two(uint32_t w, float s, float &a, float &b) {
+    const __half2_raw r = __nv_cvt_fp8x2_to_halfraw2(__nv_fp8x2_storage_t(w & 0xFFFFu), __NV_E4M3);
+    const float2 f = __half22float2(__half2(r));
+    a = f.x * s;
+    b = f.y * s;
+}
+__device__ __forceinline__ void q8_to_f(uint2 q, int e, float (&v)[8]) {
+    const float s = q8_scale(e);
+    q8_two(q.x, s, v[0], v[1]);
+    q8_two(q.x >> 16, s, v[2], v[3]);
+    q8_two(q.y, s, v[4], v[5]);
+    q8_two(q.y >> 16, s, v[6], v[7]);
+}
+
+// Stores slice `vi` of row `row` in 8 bits.  Called by every lane of the warp: the four
+// lanes of a 4-aligned run hold the four slices of one group (slices past the row's end
+// hold zeros and are not stored).
+__device__ __forceinline__ void q8_store(const float (&v)[8], bool in, uint8_t *q, uint8_t *scale, int64_t row, int c,
+                                         int vi) {
+    float m = in ? finite_amax(v) : 0.f;
+    m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+    m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+    if (!in) return;
+    const int e = q8_exponent(m);
+    *reinterpret_cast<uint2 *>(q + row * c + vi * 8) = q8_from_f(v, e);
+    if ((vi & 3) == 0) scale[row * q8_groups(c) + (vi >> 2)] = uint8_t(e);
+}
+
+// Slice `vi` of row `row` of 8-bit rows.
+__device__ __forceinline__ void q8_load(const uint8_t *q, const uint8_t *scale, int64_t row, int c, int vi, uint2 &bits,
+                                        int &e) {
+    bits = __ldg(reinterpret_cast<const uint2 *>(q + row * c + vi * 8));
+    e = __ldg(scale + row * q8_groups(c) + (vi >> 2));
+}
+
+// A value in T: fp16 ends at 65504, which a group's largest value can round past, so it
+// is held there; bf16 and fp32 have the range of the scales.
+template <typename T> __device__ __forceinline__ float in_range(float v) { return v; }
+template <> __device__ __forceinline__ float in_range<__half>(float v) {
+    return fabsf(v) > 65504.f ? copysignf(65504.f, v) : v;  // NaN stays NaN
+}
+
+// Host checks of the row-wise entry points.
+constexpr int kMaxChannels = 16384;
+inline bool chan_ok(int c) { return c >= 8 && c % 8 == 0 && c <= kMaxChannels; }
+inline bool rows_ok(int64_t n) { return n >= 0 && n < (int64_t(1) << 31); }
+inline bool aligned(const void *p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
+
+}  // namespace rows
+}  // namespace lat
