@@ -70,6 +70,9 @@ lat_status launch_wgrad_tc(bool bf16, const void *x, int cin, const void *dy, in
                            void *ws, int32_t *d_status, cudaStream_t s);
 lat_status launch_q8_unpack(const void *q, const void *scale, int64_t n, int c, void *x, lat_dtype dtype,
                             cudaStream_t s);
+size_t wgrad_q8_tc_ws_bytes(int cin, int cout, const lat_kmap *map);
+lat_status launch_wgrad_q8_tc(bool bf16, const void *q, const void *scale, int cin, const void *dy, int cout,
+                              const lat_kmap *map, float *dw, void *ws, int32_t *d_status, cudaStream_t s);
 size_t conv_tc_ws_bytes();
 lat_status launch_conv_tc(bool bf16, const void *x, int kc, const void *w, int n, int k3, const MapView &mv, bool wt,
                           void *y, void *ws, int32_t *d_status, cudaStream_t s);

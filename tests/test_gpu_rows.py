@@ -355,6 +355,56 @@ def test_weight_gradient_from_8bit_rows(n, cin, cout, dtype):
     assert torch.equal(dw, scv.conv_wgrad_q8(r, dy, km)), "the bits depend on timing"
 
 
+@pytest.mark.parametrize("cin,cout,dtype", [(64, 64, torch.bfloat16), (128, 64, torch.float16)])
+def test_weight_gradient_of_long_shares(cin, cout, dtype):
+    """A million pairs: shares of several thousand pairs of one offset, whose sums leave the accumulator more than once."""
+    coords = rand_coords(np.random.default_rng(5), 40000, -18, 18)
+    km, nbr = _subm(coords)
+    r = scv.q8_pack(_rand(1, len(coords), cin, dtype=dtype))
+    dy = _rand(2, len(coords), cout, dtype=dtype)
+    dw = scv.conv_wgrad_q8(r, dy, km)
+    x, g = values_q8(r), dy.double()
+    for k in (0, 13, 20, 26):
+        j = np.nonzero(nbr[:, k] >= 0)[0]
+        i, j = torch.from_numpy(nbr[j, k].astype(np.int64)).cuda(), torch.from_numpy(j).cuda()
+        ref, mag = x[i].t() @ g[j], x[i].abs().t() @ g[j].abs()
+        _within(dw[k], ref, (2048 + 64) * 2.0 ** -23 * mag, f"offset {k}")
+
+
+def test_weight_gradient_wait_that_runs_out():
+    """With no time to wait the kernel gives up, says so and leaves the GPU in order: the next call is right."""
+    coords = rand_coords(np.random.default_rng(6), 5000, -12, 12)
+    km, _ = _subm(coords)
+    r, dy = scv.q8_pack(_rand(1, 5000, 64, dtype=torch.bfloat16)), _rand(2, 5000, 64, dtype=torch.bfloat16)
+    want = scv.conv_wgrad_q8(r, dy, km)
+    st = scv.new_status()
+    was = scv.lat_set_wait_limit_ns(0)
+    try:
+        scv.conv_wgrad_q8(r, dy, km, d_status=st)
+        torch.cuda.synchronize()
+    finally:
+        scv.lat_set_wait_limit_ns(was)
+    with pytest.raises(scv.LatticeError, match="LAT_ERR_TIMEOUT"):
+        scv.check_status(st)
+    assert torch.equal(scv.conv_wgrad_q8(r, dy, km), want)
+
+
+def test_weight_gradient_flags_a_bad_pair():
+    """A row index outside the rows is flagged and its pair left out (the map is checked before the rows are read)."""
+    coords = rand_coords(np.random.default_rng(7), 500, -5, 5)
+    km, _ = _subm(coords)
+    for c, dtype in ((64, torch.bfloat16), (16, torch.float32)):
+        r, dy = scv.q8_pack(_rand(1, 500, c, dtype=dtype)), _rand(2, 500, c, dtype=dtype)
+        kept = km.pair_in[3].clone()
+        km.pair_in[3] = 500
+        st = scv.new_status()
+        dw = scv.conv_wgrad_q8(r, dy, km, d_status=st)
+        with pytest.raises(scv.LatticeError, match="LAT_ERR_BAD_MAP"):
+            scv.check_status(st)
+        assert bool(torch.isfinite(dw).all())
+        km.pair_in[3] = kept
+
+
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 def test_weight_gradient_from_8bit_rows_of_a_strided_map(dtype):
     """n_in and n_out differ: the coarse rows of a k=2, stride-2 convolution."""
