@@ -9,12 +9,14 @@
 // 4 significant bits and a power of two: bf16 holds it exactly.  fp16 rounds values below
 // 2^-14 to its subnormals' steps and is held at 65504.
 //
-// One CTA per SM with a ring of NS blocks of 64 pairs.  Eight warps copy the blocks' raw
-// x chunks, scale bytes and dy rows (dy straight into its swizzled tile) with cp.async
-// NS - 2 blocks ahead; each thread then widens the chunks that it copied itself -- only
-// its own cp.async groups to wait for, no barrier -- into one of two A tiles and arrives
-// at the tile's barrier, on which the MMA warp waits.  The commit of block b's MMAs frees
-// A tile b & 1 and ring slot b % NS.
+// One CTA per SM.  Two groups of eight warps take the blocks of 64 pairs in turn, each with
+// an A tile, a ring of kDy dy tiles and a ring of kRaw raw x blocks of its own.  A group
+// copies raw x chunks, scale bytes and dy rows (dy straight into its swizzled tile) with
+// cp.async three of its blocks ahead; each thread widens the chunks that it copied itself
+// -- only its own cp.async groups to wait for, no barrier -- into the A tile and arrives at
+// the tile's barrier, on which the MMA warp waits.  The commit of a block's MMAs frees the
+// A tile and the dy tile.  (One group of eight warps with two A tiles took 95 us at 500k
+// rows, 128 -> 128: a chain of latencies in two warps per scheduler.)
 //
 // A segment's sum leaves TMEM every kFlush blocks: the tensor cores cut bits off when they
 // add, and over a share of thousands of pairs in one accumulator that would be the largest
@@ -32,11 +34,14 @@ namespace wq8 {
 
 constexpr int kKP = 64;        // pairs per block (GEMM K block)
 constexpr int kWorkers = 148;  // shares of the pair list: one per B200 SM
-constexpr int kProdWarps = 8, kEpiWarps = 4;
-constexpr int kProdThreads = kProdWarps * 32;
+constexpr int kGroups = 2, kGroupWarps = 8;
+constexpr int kProdWarps = kGroups * kGroupWarps, kEpiWarps = 4;
+constexpr int kGroupThreads = kGroupWarps * 32;
+constexpr int kAhead = 3;                   // blocks that a group copies ahead
+constexpr int kDy = kAhead + 1, kRaw = kAhead;  // slots of its rings
 constexpr int kMmaWarp = kProdWarps + kEpiWarps;
 constexpr int kThreads = (kMmaWarp + 1) * 32;
-constexpr int kPairs = kKP / kProdWarps;  // pairs of a block that one warp copies
+constexpr int kPairs = kKP / kGroupWarps;  // pairs of a block that one warp copies
 constexpr int kFlush = 32;                // blocks per TMEM sum
 constexpr uint64_t kDrainNs = 1000000000ull;  // limit of the waits that drain a CTA that gave up
 
@@ -45,11 +50,10 @@ struct Cfg {
     static constexpr uint32_t kABytes = uint32_t(M) * 128;  // 64 pairs x M channels x 2 bytes
     static constexpr uint32_t kBBytes = uint32_t(N) * 128;
     static constexpr uint32_t kXBytes = uint32_t(M) * 64;   // raw
-    static constexpr int kStages = 7;
-    static constexpr uint32_t kRing = 2 * kABytes;              // A tiles, then the dy tiles, raw x, scales
-    static constexpr uint32_t kRaw = kRing + kStages * kBBytes;
-    static constexpr uint32_t kScale = kRaw + kStages * kXBytes;  // 4 bytes per pair
-    static constexpr uint32_t kBars = kScale + kStages * kKP * 4;
+    static constexpr uint32_t kDyAt = kGroups * kABytes;        // the A tiles, then the dy tiles, raw x, scales
+    static constexpr uint32_t kRawAt = kDyAt + kGroups * kDy * kBBytes;
+    static constexpr uint32_t kScaleAt = kRawAt + kGroups * kRaw * kXBytes;  // 4 bytes per pair
+    static constexpr uint32_t kBars = kScaleAt + kGroups * kRaw * kKP * 4;
     static constexpr uint32_t kSmem = kBars + 256 + 1024;
     static constexpr uint32_t kTmemCols = 2 * N;
     static constexpr int kChunks = M / 64;  // 16-byte raw chunks per thread and block
@@ -88,20 +92,19 @@ wgrad_q8_kernel(const uint8_t *__restrict__ q, const uint8_t *__restrict__ scale
                 float *__restrict__ partial, int32_t *__restrict__ ranges, uint64_t wait_ns, int32_t *d_status) {
     pdl_enter();
     using C = Cfg<M, N>;
-    constexpr int NS = C::kStages;
     constexpr uint32_t idesc = wtc::make_idesc<T, M, N>();
 
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::kBars);
-    uint64_t *empty = full + 2;
-    uint64_t *accfull = empty + 2;
+    uint64_t *empty = full + kGroups;
+    uint64_t *accfull = empty + kGroups;
     uint64_t *accempty = accfull + 2;
     uint64_t *drain = accempty + 2;  // tracks the MMAs still in flight when a CTA gives up
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
     __shared__ int s_abort;
     __shared__ int64_t s_off[33];
-    __shared__ uint8_t s_odd[NS][kKP];  // M = 64: the pair's scale bytes are the upper half of their word
+    __shared__ uint8_t s_odd[kGroups * kRaw][kKP];  // M = 64: the pair's scale bytes are the upper half of their word
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (warp == 1) {
@@ -115,9 +118,11 @@ wgrad_q8_kernel(const uint8_t *__restrict__ q, const uint8_t *__restrict__ scale
         }
     }
     if (tid == 0) {
-        for (int s = 0; s < 2; ++s) {
-            ptx::mbar_init(&full[s], kProdThreads);
+        for (int s = 0; s < kGroups; ++s) {
+            ptx::mbar_init(&full[s], kGroupThreads);
             ptx::mbar_init(&empty[s], 1);
+        }
+        for (int s = 0; s < 2; ++s) {
             ptx::mbar_init(&accfull[s], 1);
             ptx::mbar_init(&accempty[s], kEpiWarps * 32);
         }
@@ -140,13 +145,15 @@ wgrad_q8_kernel(const uint8_t *__restrict__ q, const uint8_t *__restrict__ scale
         // ------------------------------------------------------------ copy ahead, widen x
         constexpr int XL = M / 16;       // lanes per raw x row
         constexpr int XP = 32 / XL;      // rows per warp and chunk
+        const int grp = warp / kGroupWarps, gw = warp % kGroupWarps, gt = tid % kGroupThreads;
         const int xc = lane % XL, xg = lane / XL;
         const int g = lane >> 3, c = lane & 7;
         Blocks blk(s_off, k3);
         bool have = blk.next();
+        for (int i = 0; i < grp; ++i) have = have && blk.next();
         int si = -1, sj = -1;
-        auto fetch = [&]() {  // lanes 0..7: the indices of this warp's pairs of the next block
-            const int64_t mp = blk.p0 + warp * kPairs + lane;
+        auto fetch = [&]() {  // lanes 0..7: the indices of this warp's pairs of the group's next block
+            const int64_t mp = blk.p0 + gw * kPairs + lane;
             si = sj = -1;
             if (have && lane < kPairs && mp < blk.hi) {
                 si = __ldg(pair_in + mp);
@@ -155,31 +162,32 @@ wgrad_q8_kernel(const uint8_t *__restrict__ q, const uint8_t *__restrict__ scale
         };
         fetch();
         uint32_t issued = 0;
-        auto issue = [&]() {  // copies of the next block, one cp.async group (empty past the last block)
+        auto issue = [&]() {  // copies of the group's next block, one cp.async group (empty past the last block)
             if (have) {
                 if (si >= n_in || sj >= n_out || (si < 0) != (sj < 0)) {
                     bad |= LAT_ERR_BAD_MAP;
                     si = sj = -1;
                 }
-                const uint32_t s = issued % NS;
-                uint8_t *xs = smem + C::kRaw + s * C::kXBytes, *Bs = smem + C::kRing + s * C::kBBytes;
+                const uint32_t r = grp * kRaw + issued % kRaw;
+                uint8_t *xs = smem + C::kRawAt + r * C::kXBytes;
+                uint8_t *Bs = smem + C::kDyAt + (grp * kDy + issued % kDy) * C::kBBytes;
                 if (lane < kPairs) {
-                    const int p = warp * kPairs + lane;
+                    const int p = gw * kPairs + lane;
                     const int64_t at = si < 0 ? 0 : int64_t(si) * (M / 32), word = at & ~int64_t(3);
                     const int64_t left = n_in * (M / 32) - word;
-                    ptx::cp_async4(smem + C::kScale + (s * kKP + p) * 4, scale + word,
+                    ptx::cp_async4(smem + C::kScaleAt + (r * kKP + p) * 4, scale + word,
                                    si < 0 ? 0u : uint32_t(left < 4 ? left : 4));
-                    if (M == 64) s_odd[s][p] = uint8_t(at & 2);
+                    if (M == 64) s_odd[r][p] = uint8_t(at & 2);
                 }
 #pragma unroll
                 for (int i = 0; i < C::kChunks; ++i) {
                     const int ii = __shfl_sync(0xFFFFFFFFu, si, i * XP + xg);
                     const uint8_t *src = ii >= 0 ? q + int64_t(ii) * M + xc * 16 : q;
-                    ptx::cp_async16(xs + (i * kProdThreads + tid) * 16, src, ii >= 0 ? 16u : 0u);
+                    ptx::cp_async16(xs + (i * kGroupThreads + gt) * 16, src, ii >= 0 ? 16u : 0u);
                 }
 #pragma unroll
                 for (int i = 0; i < kPairs / 4; ++i) {
-                    const int pl = 4 * i + g, p = warp * kPairs + pl;
+                    const int pl = 4 * i + g, p = gw * kPairs + pl;
                     const int jj = __shfl_sync(0xFFFFFFFFu, sj, pl);
                     const uint32_t off = (p >> 3) * 1024 + (p & 7) * 128 + ((c ^ (p & 7)) << 4);
 #pragma unroll
@@ -189,33 +197,32 @@ wgrad_q8_kernel(const uint8_t *__restrict__ q, const uint8_t *__restrict__ scale
                     }
                 }
                 ++issued;
-                have = blk.next();
+                for (int i = 0; i < kGroups; ++i) have = have && blk.next();
                 fetch();
             }
             ptx::cp_async_commit();
         };
 #pragma unroll 1
-        for (int d = 0; d < NS - 2; ++d) issue();
+        for (int d = 0; d < kAhead; ++d) issue();
+        uint8_t *As = smem + grp * C::kABytes;
         bool ok = true;
 #pragma unroll 1
         for (uint32_t it = 0; it < issued; ++it) {
-            // block it - 2's MMAs: they read the A tile written here and ring slot (it - 2) % NS, refilled here
-            if (!__all_sync(0xFFFFFFFFu, ptx::mbar_wait(&empty[it & 1], ((it >> 1) & 1) ^ 1, wait_ns))) {
+            // the MMAs of the group's previous block: they read the A tile and the dy tile that issue() refills
+            if (!__all_sync(0xFFFFFFFFu, ptx::mbar_wait(&empty[grp], (it & 1) ^ 1, wait_ns))) {
                 ok = false;
                 break;
             }
-            issue();
-            ptx::cp_async_wait<NS - 2>();
+            ptx::cp_async_wait<kAhead - 1>();
             __syncwarp();
-            const uint32_t s = it % NS;
-            const uint8_t *xs = smem + C::kRaw + s * C::kXBytes;
-            const uint32_t *ss = reinterpret_cast<const uint32_t *>(smem + C::kScale) + s * kKP;
-            uint8_t *As = smem + (it & 1) * C::kABytes;
+            const uint32_t r = grp * kRaw + it % kRaw;
+            const uint8_t *xs = smem + C::kRawAt + r * C::kXBytes;
+            const uint32_t *ss = reinterpret_cast<const uint32_t *>(smem + C::kScaleAt) + r * kKP;
 #pragma unroll
             for (int i = 0; i < C::kChunks; ++i) {
-                const int p = warp * kPairs + i * XP + xg;
-                const uint4 raw = *reinterpret_cast<const uint4 *>(xs + (i * kProdThreads + tid) * 16);
-                const int shift = 8 * (xc >> 1) + (M == 64 ? 8 * s_odd[s][p] : 0);  // channels 16 xc ..
+                const int p = gw * kPairs + i * XP + xg;
+                const uint4 raw = *reinterpret_cast<const uint4 *>(xs + (i * kGroupThreads + gt) * 16);
+                const int shift = 8 * (xc >> 1) + (M == 64 ? 8 * s_odd[r][p] : 0);  // channels 16 xc ..
                 const int e = (ss[p] >> shift) & 0xFF;
                 const uint4 lo = widen<T>(make_uint2(raw.x, raw.y), e), hi = widen<T>(make_uint2(raw.z, raw.w), e);
                 // 16-byte chunks 2 xc and 2 xc + 1 of the pair's row; the upper half of the lanes stores them the
@@ -228,7 +235,9 @@ wgrad_q8_kernel(const uint8_t *__restrict__ q, const uint8_t *__restrict__ scale
             }
             // the tile and this thread's dy chunks, written through the generic proxy, before the tensor cores' reads
             ptx::fence_proxy_async_smem();
-            ptx::mbar_arrive(&full[it & 1]);
+            ptx::mbar_arrive(&full[grp]);
+            __syncwarp();  // the raw block and the scales are read: issue() refills them
+            issue();
         }
         ptx::cp_async_wait<0>();
         if (!ok) s_abort = 1;
@@ -297,13 +306,14 @@ wgrad_q8_kernel(const uint8_t *__restrict__ q, const uint8_t *__restrict__ scale
                 const int64_t end = min(hi, p + kFlush * kKP);
                 uint32_t acc = 0;
                 for (int64_t p0 = p; p0 < end; p0 += kKP) {
-                    if (!ptx::mbar_wait(&full[it & 1], (it >> 1) & 1, wait_ns)) {
+                    const uint32_t grp = it % kGroups, n = it / kGroups;  // block n of its group
+                    if (!ptx::mbar_wait(&full[grp], n & 1, wait_ns)) {
                         ok = false;
                         break;
                     }
                     ptx::tc_fence_after();
-                    const uint32_t as = ptx::smem_u32(smem + (it & 1) * C::kABytes);
-                    const uint32_t bs = ptx::smem_u32(smem + C::kRing + (it % NS) * C::kBBytes);
+                    const uint32_t as = ptx::smem_u32(smem + grp * C::kABytes);
+                    const uint32_t bs = ptx::smem_u32(smem + C::kDyAt + (grp * kDy + n % kDy) * C::kBBytes);
 #pragma unroll
                     for (int ks = 0; ks < 4; ++ks) {
                         const uint64_t ad = ptx::desc_sw128(as + ks * 2048, 8192, 1024);
@@ -311,7 +321,7 @@ wgrad_q8_kernel(const uint8_t *__restrict__ q, const uint8_t *__restrict__ scale
                         ptx::umma_f16(dcol, ad, bd, idesc, acc);
                         acc = 1;
                     }
-                    ptx::umma_commit(&empty[it & 1]);
+                    ptx::umma_commit(&empty[grp]);
                     ++it;
                 }
                 if (!ok) break;
