@@ -393,15 +393,15 @@ lat_status lat_to_dense(const int32_t *coords, int64_t n, const void *feats, int
  *           id is pad_id (any value, -1 for instance) has no token: its y is
  *           0 and its dy counts nowhere.  Another id outside [0, vocab) does
  *           the same and sets LAT_ERR_BAD_ID at d_status (may be NULL).
- *   table   device [vocab][c], y and dy device [n][c], of dtype, 16-byte
- *           aligned, without overlap; c a multiple of 8 in [8, 16384];
+ *   table   device [vocab][c], y and dy device [n][c], of dtype, aligned to
+ *           8 channels (16 bytes, fp32 32), without overlap; c a multiple of 8 in [8, 16384];
  *           n < 2^31, 1 <= vocab < 2^31 - 1.
- *   dtable  device fp32 [vocab][c], 16-byte aligned; every row is written
+ *   dtable  device fp32 [vocab][c], 32-byte aligned; every row is written
  *           (0 for a token without rows).
  * Arithmetic is fp32, one rounding to dtype.  The gradient sorts the rows by
  * token and adds each token's rows in parts whose sizes and order depend on
  * the arguments' sizes alone (no atomics on sums): its bits are the same on
- * every call.  Workspace as for the other ops (16-byte aligned); lookup
+ * every call.  Workspace as for the other ops (32-byte aligned); lookup
  * takes none.  Asynchronous on `stream`; allocates nothing. */
 lat_status lat_embed_fwd(const void *ids, int32_t id_bytes, int64_t n, const void *table, int64_t vocab,
                          int32_t c, float scale, int64_t pad_id, void *y, lat_dtype dtype,
@@ -422,8 +422,9 @@ lat_status lat_embed_wgrad(const void *ids, int32_t id_bytes, int64_t n, const v
  * 2^-6 of it).  Infinities and NaN are stored as NaN.  lat_q8_unpack writes
  * q * scale in dtype: exact in fp32 and bf16 (subnormals aside); in fp16
  * rounded to nearest and held at +-65504.
- *   x   device [n][c] of dtype; q device [n][c] bytes; both 16-byte
- *       aligned, no overlap; c a multiple of 8 in [8, 16384]; n < 2^31.
+ *   x   device [n][c] of dtype, aligned to 8 channels (16 bytes, fp32 32);
+ *       q device [n][c] bytes, 16-byte aligned; no overlap; c a multiple of
+ *       8 in [8, 16384]; n < 2^31.
  * Readers of 8-bit rows: lat_q8_unpack, lat_sconv_wgrad_q8 (the rows that a
  * convolution was given), lat_rms_norm_bwd (the rows that a norm was given).
  * Asynchronous on `stream`; allocates nothing. */
@@ -463,9 +464,9 @@ lat_status lat_rms_norm_fwd(const void *x, const void *res, const void *w, int64
  * h: the forward pass's h in dtype, or NULL and h8 / h8_scale its 8-bit rows.
  * dh: the gradient that reaches h past the norm, NULL for none.  dx may be
  * dy or dh itself; no other overlap.  The sums of dw run in a fixed order
- * over parts that depend on n and c alone.  Workspace (16-byte aligned) only
- * for dw.  Both passes: 16-byte aligned rows, c a multiple of 8 in
- * [8, 16384], n < 2^31, fp32 arithmetic; asynchronous on `stream`; they
+ * over parts that depend on n and c alone.  Workspace (32-byte aligned) only
+ * for dw.  Both passes: rows and w aligned to 8 channels (16 bytes, fp32
+ * 32), 8-bit values to 16 bytes, c a multiple of 8 in [8, 16384], n < 2^31, fp32 arithmetic; asynchronous on `stream`; they
  * allocate nothing. */
 size_t lat_rms_norm_bwd_ws_bytes(int64_t n, int32_t c);
 lat_status lat_rms_norm_bwd(const void *dy, const void *dh, const void *h, const void *h8,

@@ -62,13 +62,10 @@ lookup_kernel(const I *__restrict__ ids, int64_t n, const T *__restrict__ table,
 
 // ------------------------------------------------------------------------- the sort
 // One stable counting pass by a digit of `bits` bits: counts per (tile, digit value),
-// their scan over the tiles, and the scatter.  A tile is kTile consecutive rows; in the
-// scatter a warp takes kTile / 8 of them, 32 at a time, and ranks the rows of equal digit
-// by a warp match, so equal keys keep their order.
-constexpr int kTile = 2048;
+// their scan over the tiles, and the scatter.  A tile is a run of rows; in the
+// scatter a warp takes an eighth of them, 32 at a time, and ranks the rows of equal digit
+// by ballots, so equal keys keep their order.  A tile has kThreads * R rows.
 constexpr int kWarps = kThreads / 32;
-constexpr int kPerWarp = kTile / kWarps;
-constexpr int kRounds = kPerWarp / 32;
 constexpr int kMaxBits = 10;
 constexpr int kMaxBins = 1 << kMaxBits;
 
@@ -92,15 +89,16 @@ __device__ __forceinline__ uint32_t sort_key(const Pass &p, const Ids<I> &d, int
     return uint32_t(t < 0 ? d.vocab : t);
 }
 
-template <typename I>
+template <typename I, int R>
 __global__ void __launch_bounds__(kThreads) count_kernel(Pass p, Ids<I> d, int32_t *d_status) {
     pdl_enter();
     __shared__ uint32_t s_cnt[kMaxBins];
     const int bins = 1 << p.bits;
     for (int b = threadIdx.x; b < bins; b += kThreads) s_cnt[b] = 0;
     __syncthreads();
-    const int64_t lo = blockIdx.x * int64_t(kTile), hi = min(p.n, lo + kTile);
+    const int64_t lo = blockIdx.x * int64_t(kThreads * R), hi = min(p.n, lo + kThreads * R);
     int32_t bad = 0;
+#pragma unroll R
     for (int64_t i = lo + threadIdx.x; i < hi; i += kThreads)
         atomicAdd(&s_cnt[(sort_key(p, d, i, bad) >> p.shift) & (bins - 1)], 1u);
     __syncthreads();
@@ -140,63 +138,94 @@ __global__ void __launch_bounds__(1024) tile_scan_kernel(uint32_t *__restrict__ 
     }
 }
 
-template <typename I>
+// Inclusive sum over the lanes of a warp.
+__device__ __forceinline__ uint32_t warp_scan(uint32_t v, int lane) {
+#pragma unroll
+    for (int m = 1; m < 32; m <<= 1) {
+        const uint32_t u = __shfl_up_sync(0xFFFFFFFFu, v, m);
+        if (lane >= m) v += u;
+    }
+    return v;
+}
+
+// The lanes whose digit (`bits` bits; false `in`: none) equals this lane's, by one ballot per
+// bit.  (A warp match takes a turn per distinct value: 44 us instead of 17 for the one-block
+// sort of 16,383 rows.)
+template <int kMax>
+__device__ __forceinline__ uint32_t same_digit(uint32_t digit, int bits, bool in) {
+    uint32_t peers = __ballot_sync(0xFFFFFFFFu, in);
+#pragma unroll
+    for (int b = 0; b < kMax; ++b) {
+        if (b >= bits) break;
+        const bool one = (digit >> b) & 1u;
+        const uint32_t ones = __ballot_sync(0xFFFFFFFFu, one);
+        peers &= one ? ones : ~ones;
+    }
+    return peers;
+}
+
+template <typename I, int R>
 __global__ void __launch_bounds__(kThreads) scatter_kernel(Pass p, Ids<I> d) {
     pdl_enter();
+    constexpr int kOwn = kMaxBins / kThreads;  // digits of a thread in the scan (at most)
     __shared__ uint32_t s_cnt[kWarps][kMaxBins];
-    __shared__ uint32_t s_scan[kThreads];
+    __shared__ uint32_t s_scan[kWarps];
     const int bins = 1 << p.bits, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    for (int b = threadIdx.x; b < bins; b += kThreads)
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) s_cnt[w][b] = 0;
-    __syncthreads();
-    const int64_t lo = blockIdx.x * int64_t(kTile) + warp * kPerWarp;
-    uint32_t key[kRounds], rank[kRounds], row[kRounds];
+    const int per = (bins + kThreads - 1) / kThreads, b0 = int(threadIdx.x) * per;
+    const int64_t lo = (blockIdx.x * int64_t(kWarps) + warp) * (32 * R);
+    uint32_t key[R], rank[R], row[R], total[kOwn], start[kOwn];
     int32_t bad = 0;
 #pragma unroll
-    for (int r = 0; r < kRounds; ++r) {
+    for (int r = 0; r < R; ++r) {
         const int64_t i = lo + r * 32 + lane;
         key[r] = i < p.n ? sort_key(p, d, i, bad) : 0u;
         row[r] = i < p.n ? (p.row_in ? p.row_in[i] : uint32_t(i)) : 0u;
     }
 #pragma unroll
-    for (int r = 0; r < kRounds; ++r) {
+    for (int o = 0; o < kOwn; ++o) {
+        const bool own = o < per && b0 + o < bins;
+        total[o] = own ? p.totals[b0 + o] : 0u;
+        start[o] = own ? p.counts[int64_t(blockIdx.x) * bins + b0 + o] : 0u;
+    }
+    for (int b = threadIdx.x; b < bins; b += kThreads)
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) s_cnt[w][b] = 0;
+    // first position of each digit: an exclusive scan of the totals, a run of digits per thread
+    uint32_t sum = 0;
+#pragma unroll
+    for (int o = 0; o < kOwn; ++o) sum += total[o];
+    const uint32_t upto = warp_scan(sum, lane);
+    if (lane == 31) s_scan[warp] = upto;
+    __syncthreads();
+    uint32_t at = upto - sum;
+    for (int w = 0; w < warp; ++w) at += s_scan[w];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
         const bool in = lo + r * 32 + lane < p.n;
-        const uint32_t digit = in ? (key[r] >> p.shift) & (bins - 1) : uint32_t(bins);
-        const uint32_t peers = __match_any_sync(0xFFFFFFFFu, digit);
+        const uint32_t digit = (key[r] >> p.shift) & (bins - 1);
+        const uint32_t peers = same_digit<kMaxBits>(digit, p.bits, in);
         const uint32_t before = __popc(peers & ((1u << lane) - 1u));
         if (in) rank[r] = s_cnt[warp][digit] + before;
         __syncwarp();
         if (in && before == 0) s_cnt[warp][digit] += __popc(peers);
         __syncwarp();
     }
-    // first position of each digit: an exclusive scan of the totals, a run of digits per thread
-    const int per = (bins + kThreads - 1) / kThreads;
-    const int b0 = min(bins, int(threadIdx.x) * per), b1 = min(bins, b0 + per);
-    uint32_t sum = 0;
-    for (int b = b0; b < b1; ++b) sum += p.totals[b];
-    s_scan[threadIdx.x] = sum;
     __syncthreads();
-    for (int m = 1; m < kThreads; m <<= 1) {
-        const uint32_t v = int(threadIdx.x) >= m ? s_scan[threadIdx.x - m] : 0u;
-        __syncthreads();
-        s_scan[threadIdx.x] += v;
-        __syncthreads();
-    }
-    uint32_t at = threadIdx.x ? s_scan[threadIdx.x - 1] : 0u;
-    for (int b = b0; b < b1; ++b) {
-        uint32_t run = at + p.counts[int64_t(blockIdx.x) * bins + b];
-        at += p.totals[b];
+#pragma unroll
+    for (int o = 0; o < kOwn; ++o) {
+        if (o >= per || b0 + o >= bins) break;
+        uint32_t run = at + start[o];
+        at += total[o];
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
-            const uint32_t v = s_cnt[w][b];
-            s_cnt[w][b] = run;
+            const uint32_t v = s_cnt[w][b0 + o];
+            s_cnt[w][b0 + o] = run;
             run += v;
         }
     }
     __syncthreads();
 #pragma unroll
-    for (int r = 0; r < kRounds; ++r) {
+    for (int r = 0; r < R; ++r) {
         if (lo + r * 32 + lane < p.n) {
             const uint32_t pos = s_cnt[warp][(key[r] >> p.shift) & (bins - 1)] + rank[r];
             p.key_out[pos] = key[r];
@@ -205,11 +234,110 @@ __global__ void __launch_bounds__(kThreads) scatter_kernel(Pass p, Ids<I> d) {
     }
 }
 
+// All passes of up to kSmall rows by one block, in shared memory: the same ranks, with the
+// counts of (digit value, warp) scanned in that order.  (One SM's issue slots bound it: at
+// 16,383 rows it took 38 us, more than the passes above.)
+constexpr int kSmall = 4096, kSmallThreads = 1024, kSmallWarps = kSmallThreads / 32;
+constexpr int kSmallRounds = kSmall / kSmallThreads, kSmallBits = 8, kSmallBins = 1 << kSmallBits;
+constexpr int kCntStride = kSmallWarps + 1;
+constexpr size_t kSmallSmem = kSmall * 4 + kSmall * 2 + kSmallBins * kCntStride * 2 + 16;
+template <typename I>
+__global__ void __launch_bounds__(kSmallThreads)
+sort_small_kernel(Ids<I> d, int n, int bits, uint32_t *__restrict__ key_out, uint32_t *__restrict__ row_out,
+                  int32_t *__restrict__ open_count, int32_t *d_status) {
+    pdl_enter();
+    extern __shared__ __align__(16) uint8_t smem[];
+    uint32_t *s_key = reinterpret_cast<uint32_t *>(smem);
+    uint16_t *s_row = reinterpret_cast<uint16_t *>(smem + kSmall * 4);
+    uint16_t *s_cnt = s_row + kSmall;
+    __shared__ uint32_t s_scan[kSmallWarps];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rounds = (n + kSmallThreads - 1) / kSmallThreads, lo = warp * rounds * 32;
+    if (threadIdx.x == 0) *open_count = 0;
+    uint32_t key[kSmallRounds], row[kSmallRounds];  // row: and the rank, in the upper half
+    int32_t bad = 0;
+#pragma unroll
+    for (int r = 0; r < kSmallRounds; ++r) {
+        const int i = lo + r * 32 + lane;
+        if (r < rounds && i < n) {
+            const int64_t t = token(d.ids, i, d.vocab, d.pad, bad);
+            key[r] = uint32_t(t < 0 ? d.vocab : t);
+            row[r] = uint32_t(i);
+        }
+    }
+    for (int shift = 0; shift < bits; shift += kSmallBits) {
+        for (int b = threadIdx.x; b < kSmallBins * kCntStride / 2; b += kSmallThreads)
+            reinterpret_cast<uint32_t *>(s_cnt)[b] = 0;
+        __syncthreads();
+#pragma unroll
+        for (int r = 0; r < kSmallRounds; ++r) {
+            if (r >= rounds) break;
+            const bool in = lo + r * 32 + lane < n;
+            const uint32_t digit = in ? (key[r] >> shift) & (kSmallBins - 1) : 0u;
+            const uint32_t peers = same_digit<kSmallBits>(digit, kSmallBits, in);
+            const uint32_t before = __popc(peers & ((1u << lane) - 1u));
+            uint16_t *cnt = s_cnt + digit * kCntStride + warp;
+            if (in) row[r] = (row[r] & 0xFFFFu) | ((*cnt + before) << 16);
+            __syncwarp();
+            if (in && before == 0) *cnt += uint16_t(__popc(peers));
+            __syncwarp();
+        }
+        __syncthreads();
+        constexpr int kOwn = kSmallBins * kSmallWarps / kSmallThreads;  // a thread's counts, in (digit, warp) order
+        uint16_t *own = s_cnt + threadIdx.x * kOwn / kSmallWarps * kCntStride + threadIdx.x * kOwn % kSmallWarps;
+        uint32_t sum = 0, c[kOwn];
+#pragma unroll
+        for (int o = 0; o < kOwn; ++o) {
+            c[o] = own[o];
+            sum += c[o];
+        }
+        const uint32_t upto = warp_scan(sum, lane);
+        if (lane == 31) s_scan[warp] = upto;
+        __syncthreads();
+        const uint32_t base = lane < warp ? s_scan[lane] : 0u;
+        uint32_t at = upto - sum + __reduce_add_sync(0xFFFFFFFFu, base);
+#pragma unroll
+        for (int o = 0; o < kOwn; ++o) {
+            own[o] = uint16_t(at);
+            at += c[o];
+        }
+        __syncthreads();
+#pragma unroll
+        for (int r = 0; r < kSmallRounds; ++r) {
+            if (r < rounds && lo + r * 32 + lane < n) {
+                const uint32_t pos =
+                    s_cnt[((key[r] >> shift) & (kSmallBins - 1)) * kCntStride + warp] + (row[r] >> 16);
+                s_key[pos] = key[r];
+                s_row[pos] = uint16_t(row[r]);
+            }
+        }
+        __syncthreads();
+#pragma unroll
+        for (int r = 0; r < kSmallRounds; ++r) {
+            const int i = lo + r * 32 + lane;
+            if (r < rounds && i < n) {
+                key[r] = s_key[i];
+                row[r] = s_row[i];
+            }
+        }
+        // the next pass writes s_key again only after its own barriers
+    }
+#pragma unroll
+    for (int r = 0; r < kSmallRounds; ++r) {
+        const int i = lo + r * 32 + lane;
+        if (r < rounds && i < n) {
+            key_out[i] = key[r];
+            row_out[i] = row[r];
+        }
+    }
+    if (bad) flag(d_status, bad);
+}
+
 // ------------------------------------------------------------------------ the sums
 struct Path {
     const uint32_t *key, *row;  // sorted
-    int64_t n, vocab;
-    int64_t share;              // steps per share
+    uint32_t n, vocab;          // steps: n + vocab < 2^32
+    uint32_t share;             // steps per share
     int shares;
     int c;
     float scale;
@@ -218,114 +346,165 @@ struct Path {
     float *dtable;
 };
 
-// Sorted rows among the first `step` steps of the path: the first i with key[i] + i >= step
-// (key[i] + i increases strictly).  W lanes search together: each round splits the range
-// into W + 1 parts.
-template <int W>
-__device__ __forceinline__ int64_t path_rows(const Path &p, int64_t step, int lane, uint32_t mask, int first) {
-    int64_t lo = max(int64_t(0), step - p.vocab), hi = min(step, p.n);  // the answer is in [lo, hi]
+// First index in [lo, hi) at which `before` no longer holds (hi if it holds everywhere).  W
+// lanes of a group (mask, first: its lanes in the warp) search together: each round splits
+// the range into W + 1 parts, so 500,000 rows take four dependent reads with 32 lanes.
+template <int W, typename F>
+__device__ __forceinline__ uint32_t first_not(uint32_t lo, uint32_t hi, int lane, uint32_t mask, int first, F &&before) {
     while (lo < hi) {
-        const int64_t span = hi - lo;
-        const int64_t at = lo + span * (lane + 1) / (W + 1);  // in [lo, hi)
-        const bool less = int64_t(p.key[at]) + at < step;
-        const uint32_t votes = (__ballot_sync(mask, less) & mask) >> first;
-        const int k = __popc(votes);  // the probes are in order, so the votes are a prefix
-        const int64_t nlo = k == 0 ? lo : lo + span * k / (W + 1) + 1;
-        const int64_t nhi = k == W ? hi : lo + span * (k + 1) / (W + 1);
+        const uint32_t span = hi - lo;
+        auto part = [&](uint32_t k) { return lo + uint32_t(uint64_t(span) * k / (W + 1)); };
+        // the probes are in order, so the votes are a prefix
+        const int k = __popc((__ballot_sync(mask, before(part(lane + 1))) & mask) >> first);
+        const uint32_t nlo = k == 0 ? lo : part(k) + 1, nhi = k == W ? hi : part(k + 1);
         lo = nlo;
         hi = nhi;
     }
     return lo;
 }
 
+// Sorted rows among the first `step` steps of the path: the first i with key[i] + i >= step
+// (key[i] + i increases strictly).
+template <int W>
+__device__ __forceinline__ uint32_t path_rows(const Path &p, uint32_t step, int lane, uint32_t mask, int first) {
+    return first_not<W>(step > p.vocab ? step - p.vocab : 0u, min(step, p.n), lane, mask, first,
+                        [&](uint32_t at) { return uint64_t(__ldg(p.key + at)) + at < step; });
+}
+
+// A group's lanes read the tokens and rows of L steps at a time, one step each, and the next
+// ones before they add; kFlight rows of dy are in flight while kFlight are added.  A block
+// takes kThreads / L consecutive shares; if a token's run covers them all, their sums meet in
+// shared memory and the first share's head stands for the block.
 template <typename T, int L>
-__global__ void __launch_bounds__(kThreads) sums_kernel(Path p, const T *__restrict__ dy) {
+__global__ void __launch_bounds__(kThreads, 3) sums_kernel(Path p, const T *__restrict__ dy) {
     pdl_enter();
-    constexpr int U = sizeof(T) == 2 ? 8 : 4;  // rows in flight
+    constexpr int kGroups = kThreads / L;
+    constexpr int kFlight = sizeof(T) == 4 || L == 4 ? 2 : 4;  // an even number of times per batch
+    __shared__ float s_acc[8][kThreads];
     const int group = threadIdx.x / L, lane = threadIdx.x % L, first = (threadIdx.x & 31) / L * L;
-    const uint32_t mask = (L == 32 ? 0xFFFFFFFFu : ((1u << L) - 1u) << first);
-    const int v = blockIdx.x * (kThreads / L) + group;
-    if (v >= p.shares) return;
-    const int64_t s0 = v * p.share, s1 = min(s0 + p.share, p.vocab + p.n);
-    const int64_t i0 = path_rows<L>(p, s0, lane, mask, first), i1 = path_rows<L>(p, s1, lane, mask, first);
-    const int64_t r0 = s0 - i0, r1 = s1 - i1;
+    const uint32_t mask = (L == 32 ? 0xFFFFFFFFu : ((1u << (L & 31)) - 1u) << first);
+    const int v = blockIdx.x * kGroups + group;
+    const uint32_t steps = p.vocab + p.n;
+    const uint32_t s0 = uint32_t(min(uint64_t(v) * p.share, uint64_t(steps)));
+    const uint32_t s1 = uint32_t(min(uint64_t(s0) + p.share, uint64_t(steps)));
+    const uint32_t i0 = path_rows<L>(p, s0, lane, mask, first), i1 = path_rows<L>(p, s1, lane, mask, first);
+    const uint32_t r0 = s0 - i0, r1 = s1 - i1;
     const int vi = blockIdx.y * L + lane;
-    if (vi >= p.c / 8) return;
-    const int64_t col = vi * 8;
-    // the first token's run began in an earlier share
-    const bool cut = i0 > 0 && int64_t(p.key[i0 - 1]) == r0;
+    const bool own = vi < p.c / 8;
+    const uint32_t col = vi * 8;
+    // the first token's run began in an earlier share; the last token's run goes on in the next one
+    const bool cut = i0 > 0 && __ldg(p.key + i0 - 1) == r0;
+    const bool goes_on = r1 < p.vocab && i1 > 0 && __ldg(p.key + i1 - 1) == r1;
     float acc[8] = {};
-    int64_t r = r0;
+    uint32_t r = r0;
     auto store = [&]() {
-        if (cut && r == r0) {
-            rows::st(p.head + v * int64_t(p.c) + col, acc);
-        } else {
+        if (own) {
+            if (cut && r == r0) {
+                rows::st(p.head + v * int64_t(p.c) + col, acc);
+            } else {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) acc[e] *= p.scale;
-            rows::st(p.dtable + r * p.c + col, acc);
+                for (int e = 0; e < 8; ++e) acc[e] *= p.scale;
+                rows::st(p.dtable + int64_t(r) * p.c + col, acc);
+            }
         }
 #pragma unroll
         for (int e = 0; e < 8; ++e) acc[e] = 0.f;
         ++r;
     };
-    for (int64_t b = i0; b < i1; b += U) {
-        int64_t key[U];
-        Slice8<T> x[U];
+    auto go_to = [&](uint32_t t) {  // the path's stores up to token t
+        if (r >= t) return;
+        store();
+        if (r >= t) return;
+        float *at = p.dtable + int64_t(r) * p.c + col;
+        for (; r < t; ++r, at += p.c)
+            if (own) rows::st(at, acc);  // tokens without rows: zeros
+    };
+    // a step past the share's end, and a row without a token, adds nothing
+    auto step_key = [&](uint32_t i) { return i < i1 ? __ldg(p.key + i) : p.vocab; };
+    auto step_row = [&](uint32_t i) { return i < i1 ? __ldg(p.row + i) : 0u; };
+    uint32_t key = step_key(i0 + lane), row = step_row(i0 + lane), next_key = 0, next_row = 0;
+    Slice8<T> x[2][kFlight];
+    auto load = [&](Slice8<T> (&to)[kFlight], uint32_t keys, uint32_t rows_, int q) {
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            key[u] = b + u < i1 ? int64_t(p.key[b + u]) : p.vocab;
-            x[u] = key[u] < p.vocab ? rows::ld(dy + int64_t(p.row[b + u]) * p.c + col) : rows::zero_slice<T>();
+        for (int u = 0; u < kFlight; ++u) {
+            const uint32_t t = __shfl_sync(mask, keys, (q + u) % L, L), at = __shfl_sync(mask, rows_, (q + u) % L, L);
+            to[u] = own && t < p.vocab ? rows::ld(dy + int64_t(at) * p.c + col) : rows::zero_slice<T>();
         }
+    };
+    load(x[0], key, row, 0);
+    for (uint32_t b = i0; b < i1; b += L) {
+        next_key = step_key(b + L + lane);
+        next_row = step_row(b + L + lane);
+        // steps of this batch that begin a new token (bit: the step)
+        const uint32_t before = __shfl_up_sync(mask, key, 1, L);
+        const uint32_t begins = (__ballot_sync(mask, (lane == 0 || key != before) && key < p.vocab) & mask) >> first;
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            if (b + u >= i1) break;
-            while (r < key[u] && r < p.vocab) store();
-            float f[8];
-            rows::to_f(x[u], f);
+        for (int q = 0; q < L; q += kFlight) {
+            const int now = (q / kFlight) & 1;
+            if (b + q >= i1) break;
+            if (q + kFlight < L) load(x[now ^ 1], key, row, q + kFlight);
+            else load(x[now ^ 1], next_key, next_row, 0);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) acc[e] += f[e];
+            for (int u = 0; u < kFlight; ++u) {
+                if ((begins >> (q + u)) & 1u) go_to(__shfl_sync(mask, key, q + u, L));
+                float f[8];
+                rows::to_f(x[now][u], f);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) acc[e] += f[e];
+            }
         }
+        key = next_key;
+        row = next_row;
     }
-    while (r < r1) store();
-    // the last token's run goes on in the next share
-    if (r < p.vocab && i1 > 0 && int64_t(p.key[i1 - 1]) == r) {
-        const bool begun_before = cut && r == r0;
-        rows::st((begun_before ? p.head : p.tail) + v * int64_t(p.c) + col, acc);
-        if (!begun_before && vi == 0) p.open[atomicAdd(p.open_count, 1)] = v;
+    go_to(r1);
+    const bool through = cut && goes_on && r == r0;  // the share lies inside one token's run
+    if (__syncthreads_and(through)) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s_acc[e][threadIdx.x] = acc[e];
+        __syncthreads();
+        if (group == 0 && own) {
+            for (int g = 1; g < kGroups; ++g)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) acc[e] += s_acc[e][g * L + lane];
+            rows::st(p.head + v * int64_t(p.c) + col, acc);
+        }
+    } else if (goes_on && own) {
+        rows::st((through ? p.head : p.tail) + v * int64_t(p.c) + col, acc);
+        if (!through && vi == 0) p.open[atomicAdd(p.open_count, 1)] = v;
     }
 }
 
-// Tokens whose run crosses a cut: for each listed share v a block adds tail[v], head[v + 1],
-// ..., up to the share that holds the run's end: row t of kJoinRows takes the shares v + t,
-// v + t + kJoinRows, ... in order, then the rows' sums are added in order.  The list's order
+// Tokens whose run crosses a cut: for each listed share v the run is tail[v], then the heads
+// of the shares up to the one that holds the run's end, where a sums block that lies between
+// v's and the last one's has one head for all its shares.  Row t of kJoinRows adds the parts
+// t, t + kJoinRows, ... in order, then the rows' sums are added in order.  The list's order
 // does not matter: every token is the sum of one entry.
-constexpr int kJoinRows = 16, kJoinBlocks = 592;
-__global__ void __launch_bounds__(32 * kJoinRows) join_kernel(Path p) {
+constexpr int kJoinRows = 8, kJoinBlocks = 1184;
+__global__ void __launch_bounds__(32 * kJoinRows) join_kernel(Path p, int per_block) {
     pdl_enter();
     __shared__ int s_last;
-    __shared__ int64_t s_row;
+    __shared__ uint32_t s_row;
     __shared__ float4 s[kJoinRows][32];
     const int count = *p.open_count;
     for (int o = blockIdx.x; o < count; o += gridDim.x) {
         const int v = p.open[o];
         if (threadIdx.y == 0) {
             const int lane = threadIdx.x;
-            const int64_t s1 = (v + 1) * p.share, i1 = path_rows<32>(p, s1, lane, 0xFFFFFFFFu, 0), r = s1 - i1;
-            int64_t lo = i1, hi = p.n;  // the first sorted row past the run of token r
-            while (lo < hi) {
-                const int64_t span = hi - lo, at = lo + span * (lane + 1) / 33;
-                const int k = __popc(__ballot_sync(0xFFFFFFFFu, int64_t(p.key[at]) <= r));
-                const int64_t nlo = k == 0 ? lo : lo + span * k / 33 + 1, nhi = k == 32 ? hi : lo + span * (k + 1) / 33;
-                lo = nlo;
-                hi = nhi;
-            }
+            const uint32_t s1 = (v + 1) * p.share, i1 = path_rows<32>(p, s1, lane, 0xFFFFFFFFu, 0), r = s1 - i1;
+            // the first sorted row past the run of token r
+            const uint32_t lo = first_not<32>(i1, p.n, lane, 0xFFFFFFFFu, 0,
+                                              [&](uint32_t at) { return __ldg(p.key + at) <= r; });
             if (lane == 0) {
-                s_last = int((lo + r) / p.share);  // the share of the step that stores the token
+                s_last = int((uint64_t(lo) + r) / p.share);  // the share of the step that stores the token
                 s_row = r;
             }
         }
         __syncthreads();
         const int last = s_last;
+        // shares v .. end of v's block, whole blocks, then the shares of the last block
+        const int block = v / per_block, blocks = max(0, last / per_block - block - 1);
+        const int lead = min(last, (block + 1) * per_block - 1) - v + 1;
+        const int parts = blocks > 0 ? lead + blocks + last % per_block + 1 : last - v + 1;
         const int col = (blockIdx.y * 32 + threadIdx.x) * 4;
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
         auto add = [&](const float4 &x) {
@@ -336,15 +515,19 @@ __global__ void __launch_bounds__(32 * kJoinRows) join_kernel(Path p) {
         };
         if (col < p.c) {
 #pragma unroll 4
-            for (int q = v + threadIdx.y; q <= last; q += kJoinRows)
-                add(*reinterpret_cast<const float4 *>((q == v ? p.tail : p.head) + q * int64_t(p.c) + col));
+            for (int q = threadIdx.y; q < parts; q += kJoinRows) {
+                int64_t at = v + q;
+                if (blocks > 0 && q >= lead)
+                    at = q < lead + blocks ? (block + 1 + q - lead) * per_block : last - (parts - 1 - q);
+                add(*reinterpret_cast<const float4 *>((q == 0 ? p.tail : p.head) + at * p.c + col));
+            }
         }
         s[threadIdx.y][threadIdx.x] = acc;
         __syncthreads();
         if (threadIdx.y == 0 && col < p.c) {
 #pragma unroll
             for (int q = 1; q < kJoinRows; ++q) add(s[q][threadIdx.x]);
-            *reinterpret_cast<float4 *>(p.dtable + s_row * p.c + col) =
+            *reinterpret_cast<float4 *>(p.dtable + int64_t(s_row) * p.c + col) =
                 make_float4(acc.x * p.scale, acc.y * p.scale, acc.z * p.scale, acc.w * p.scale);
         }
         __syncthreads();
@@ -368,10 +551,10 @@ static lat_status by_lanes(int c, F &&f) {
     return f(std::integral_constant<int, 32>{});
 }
 
-// Shares of the path: enough groups for every warp slot of a B200, but at least 16 steps
-// each; the numbers depend on the sizes alone.
+// Shares of the path: one wave of groups (the sums' registers admit 24 warps on each of a
+// B200's 148 SMs), but at least 16 steps each; the numbers depend on the sizes alone.
 static int path_shares(int64_t n, int64_t vocab, int c) {
-    const int64_t slabs = (c / 8 + 31) / 32, want = 148 * 32 * (32 / lanes_of(c)) / slabs;
+    const int64_t slabs = (c / 8 + 31) / 32, want = 148 * 24 * (32 / lanes_of(c)) / slabs;
     return int(std::max<int64_t>(1, std::min<int64_t>(want, (n + vocab + 15) / 16)));
 }
 
@@ -379,6 +562,14 @@ static int key_bits(int64_t vocab) {
     int b = 1;
     while ((int64_t(1) << b) <= vocab) ++b;  // keys 0 .. vocab
     return b;
+}
+
+// Rows per thread of the sort's tiles: small tiles while there are few rows, so that enough
+// SMs sort; large ones later, so that the counts stay few.
+static int tile_rounds(int64_t n) { return n <= 65536 ? 2 : 8; }
+static int64_t tiles_of(int64_t n) {
+    const int64_t tile = kThreads * tile_rounds(n);
+    return (n + tile - 1) / tile;
 }
 
 struct Ws {
@@ -392,7 +583,7 @@ struct Ws {
             key[i] = cv.take<uint32_t>(size_t(n));
             row[i] = cv.take<uint32_t>(size_t(n));
         }
-        counts = cv.take<uint32_t>(size_t((n + kTile - 1) / kTile) * kMaxBins);
+        counts = cv.take<uint32_t>(size_t(tiles_of(n)) * kMaxBins);
         totals = cv.take<uint32_t>(kMaxBins);
         const size_t part = size_t(path_shares(n, vocab, c)) * size_t(c);
         head = cv.take<float>(part);
@@ -407,24 +598,32 @@ lat_status wgrad(const I *ids, int64_t n, const T *dy, int64_t vocab, int c, flo
                  void *ws, int32_t *d_status, cudaStream_t s) {
     Ws w(ws, n, vocab, c);
     int at = 0;
-    if (n > 0) {
+    if (n > 0 && n <= kSmall) {
+        auto kern = sort_small_kernel<I>;
+        LAT_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kSmallSmem)));
+        LAT_CUDA_TRY(launch_pdl(kern, dim3(1), dim3(kSmallThreads), kSmallSmem, s, Ids<I>{ids, vocab, pad}, int(n),
+                                key_bits(vocab), w.key[0], w.row[0], w.open, d_status));
+    } else if (n > 0) {
         const int bits = key_bits(vocab), passes = (bits + kMaxBits - 1) / kMaxBits, digit = (bits + passes - 1) / passes;
-        const int tiles = int((n + kTile - 1) / kTile), bins = 1 << digit;
+        const int tiles = int(tiles_of(n)), bins = 1 << digit;
+        const bool few = tile_rounds(n) == 2;
+        auto count = few ? count_kernel<I, 2> : count_kernel<I, 8>;
+        auto scatter = few ? scatter_kernel<I, 2> : scatter_kernel<I, 8>;
         const Ids<I> d{ids, vocab, pad};
         for (int i = 0; i < passes; ++i) {
             const int to = i & 1;
             Pass p{i ? w.key[1 - to] : nullptr, i ? w.row[1 - to] : nullptr, w.key[to], w.row[to], w.counts, w.totals, n,
                    tiles, i * digit, digit};
-            LAT_CUDA_TRY(launch_pdl(count_kernel<I>, dim3(tiles), dim3(kThreads), 0, s, p, d, i ? nullptr : d_status));
+            LAT_CUDA_TRY(launch_pdl(count, dim3(tiles), dim3(kThreads), 0, s, p, d, i ? nullptr : d_status));
             LAT_CUDA_TRY(launch_pdl(tile_scan_kernel, dim3((bins + 31) / 32), dim3(32, 32), 0, s, w.counts, w.totals,
                                     tiles, bins, w.open));
-            LAT_CUDA_TRY(launch_pdl(scatter_kernel<I>, dim3(tiles), dim3(kThreads), 0, s, p, d));
+            LAT_CUDA_TRY(launch_pdl(scatter, dim3(tiles), dim3(kThreads), 0, s, p, d));
             at = to;
         }
     }
-    Path p{w.key[at], w.row[at], n, vocab, 0, path_shares(n, vocab, c), c, scale, w.head, w.tail,
+    Path p{w.key[at], w.row[at], uint32_t(n), uint32_t(vocab), 0, path_shares(n, vocab, c), c, scale, w.head, w.tail,
            w.open + 1, w.open, dtable};
-    p.share = (n + vocab + p.shares - 1) / p.shares;
+    p.share = uint32_t((n + vocab + p.shares - 1) / p.shares);
     const lat_status st = by_lanes(c, [&](auto l) -> lat_status {
         constexpr int L = decltype(l)::value;
         const dim3 grid(unsigned((p.shares + kThreads / L - 1) / (kThreads / L)), unsigned((c / 8 + L - 1) / L));
@@ -433,7 +632,7 @@ lat_status wgrad(const I *ids, int64_t n, const T *dy, int64_t vocab, int c, flo
     });
     if (st != LAT_OK || n == 0) return st;
     LAT_CUDA_TRY(launch_pdl(join_kernel, dim3(unsigned(std::min(p.shares, kJoinBlocks)), unsigned((c + 127) / 128)),
-                            dim3(32, kJoinRows), 0, s, p));
+                            dim3(32, kJoinRows), 0, s, p, kThreads / lanes_of(c)));
     return LAT_OK;
 }
 
@@ -478,7 +677,7 @@ extern "C" lat_status lat_embed_fwd(const void *ids, int32_t id_bytes, int64_t n
                                     int32_t *d_status, lat_stream stream) {
     using namespace lat;
     if (!embed::args_ok(ids, id_bytes, n, vocab, c, dtype) || !table || (n > 0 && !y)) return LAT_ERR_ARG;
-    if (!rows::aligned(table, 16) || !rows::aligned(y, 16)) return LAT_ERR_ARG;
+    if (!rows::aligned(table, rows::slice_bytes(dtype)) || !rows::aligned(y, rows::slice_bytes(dtype))) return LAT_ERR_ARG;
     if (n == 0) return LAT_OK;
     return embed::by_types(ids, id_bytes, dtype, [&](auto id, auto e) {
         using T = decltype(e);
@@ -498,8 +697,8 @@ extern "C" lat_status lat_embed_wgrad(const void *ids, int32_t id_bytes, int64_t
                                       size_t ws_bytes, int32_t *d_status, lat_stream stream) {
     using namespace lat;
     if (!embed::args_ok(ids, id_bytes, n, vocab, c, dtype) || !dtable || (n > 0 && !dy)) return LAT_ERR_ARG;
-    if (!rows::aligned(dy, 16) || !rows::aligned(dtable, 16)) return LAT_ERR_ARG;
-    if (!ws || !rows::aligned(ws, 16) || ws_bytes < lat_embed_wgrad_ws_bytes(n, vocab, c)) return LAT_ERR_WORKSPACE;
+    if (!rows::aligned(dy, rows::slice_bytes(dtype)) || !rows::aligned(dtable, 32)) return LAT_ERR_ARG;
+    if (!ws || !rows::aligned(ws, 32) || ws_bytes < lat_embed_wgrad_ws_bytes(n, vocab, c)) return LAT_ERR_WORKSPACE;
     return embed::by_types(ids, id_bytes, dtype, [&](auto id, auto e) {
         using T = decltype(e);
         return embed::wgrad(id, n, static_cast<const T *>(dy), vocab, c, scale, pad_id, dtable, ws, d_status,

@@ -207,7 +207,11 @@ __global__ void __launch_bounds__(L == 0 ? 1024 : kThreads) norm_bwd_kernel(Bwd<
     } else {
 #pragma unroll
         for (int k = 0; k < K; ++k)
-            if (lane + k * lanes < slices) rows::st(s_dw + group * a.c + (lane + k * lanes) * 8, dw[k]);
+            if (lane + k * lanes < slices) {
+                float4 *d = reinterpret_cast<float4 *>(s_dw + group * a.c + (lane + k * lanes) * 8);
+                d[0] = make_float4(dw[k][0], dw[k][1], dw[k][2], dw[k][3]);
+                d[1] = make_float4(dw[k][4], dw[k][5], dw[k][6], dw[k][7]);
+            }
         __syncthreads();
         for (int c = threadIdx.x; c < a.c; c += kThreads) {
             float t = 0.f;
@@ -314,9 +318,9 @@ extern "C" lat_status lat_rms_norm_fwd(const void *x, const void *res, const voi
     if (dtype != LAT_F32 && dtype != LAT_F16 && dtype != LAT_BF16) return LAT_ERR_ARG;
     if (!y8 != !y8_scale || !h8 != !h8_scale) return LAT_ERR_ARG;
     if (n > 0 && !x) return LAT_ERR_ARG;
-    for (const void *p : {x, res, w, static_cast<const void *>(h), static_cast<const void *>(y),
-                          static_cast<const void *>(y8), static_cast<const void *>(h8)})
-        if (!rows::aligned(p, 16)) return LAT_ERR_ARG;
+    for (const void *p : {x, res, w, static_cast<const void *>(h), static_cast<const void *>(y)})
+        if (!rows::aligned(p, rows::slice_bytes(dtype))) return LAT_ERR_ARG;
+    if (!rows::aligned(y8, 16) || !rows::aligned(h8, 16)) return LAT_ERR_ARG;
     if (n == 0) return LAT_OK;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     switch (dtype) {
@@ -343,9 +347,10 @@ extern "C" lat_status lat_rms_norm_bwd(const void *dy, const void *dh, const voi
     if (dtype != LAT_F32 && dtype != LAT_F16 && dtype != LAT_BF16) return LAT_ERR_ARG;
     if (!h8 != !h8_scale || (h && h8)) return LAT_ERR_ARG;
     if (n > 0 && (!dy || !rstd || !dx || (!h && !h8))) return LAT_ERR_ARG;
-    for (const void *p : {dy, dh, h, h8, w, static_cast<const void *>(dx), static_cast<const void *>(dw)})
-        if (!rows::aligned(p, 16)) return LAT_ERR_ARG;
-    if (dw && (!ws || !rows::aligned(ws, 16) || ws_bytes < lat_rms_norm_bwd_ws_bytes(n, c))) return LAT_ERR_WORKSPACE;
+    for (const void *p : {dy, dh, h, w, static_cast<const void *>(dx)})
+        if (!rows::aligned(p, rows::slice_bytes(dtype))) return LAT_ERR_ARG;
+    if (!rows::aligned(h8, 16) || !rows::aligned(dw, 4)) return LAT_ERR_ARG;
+    if (dw && (!ws || !rows::aligned(ws, 32) || ws_bytes < lat_rms_norm_bwd_ws_bytes(n, c))) return LAT_ERR_WORKSPACE;
     if (n == 0 && !dw) return LAT_OK;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     float *partial = static_cast<float *>(ws);

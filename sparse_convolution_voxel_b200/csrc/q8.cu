@@ -98,7 +98,7 @@ extern "C" lat_status lat_q8_pack(const void *x, int64_t n, int32_t c, void *q, 
     if (!rows::rows_ok(n) || !rows::chan_ok(c)) return LAT_ERR_ARG;
     if (dtype != LAT_F32 && dtype != LAT_F16 && dtype != LAT_BF16) return LAT_ERR_ARG;
     if (n > 0 && (!x || !q || !scale)) return LAT_ERR_ARG;
-    if (!rows::aligned(x, 16) || !rows::aligned(q, 16)) return LAT_ERR_ARG;
+    if (!rows::aligned(x, rows::slice_bytes(dtype)) || !rows::aligned(q, 16)) return LAT_ERR_ARG;
     if (n == 0) return LAT_OK;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     uint8_t *qb = static_cast<uint8_t *>(q), *sb = static_cast<uint8_t *>(scale);
@@ -116,6 +116,6 @@ extern "C" lat_status lat_q8_unpack(const void *q, const void *scale, int64_t n,
     if (!rows::rows_ok(n) || !rows::chan_ok(c)) return LAT_ERR_ARG;
     if (dtype != LAT_F32 && dtype != LAT_F16 && dtype != LAT_BF16) return LAT_ERR_ARG;
     if (n > 0 && (!x || !q || !scale)) return LAT_ERR_ARG;
-    if (!rows::aligned(x, 16) || !rows::aligned(q, 16)) return LAT_ERR_ARG;
+    if (!rows::aligned(x, rows::slice_bytes(dtype)) || !rows::aligned(q, 16)) return LAT_ERR_ARG;
     return launch_q8_unpack(q, scale, n, c, x, dtype, reinterpret_cast<cudaStream_t>(stream));
 }

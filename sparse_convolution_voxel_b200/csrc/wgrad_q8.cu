@@ -77,11 +77,10 @@ template <typename T>
 __device__ __forceinline__ uint4 widen(uint2 q, int e) {
     float v[8];
     rows::q8_to_f(q, e, v);
-    uint4 o;
-    T *t = reinterpret_cast<T *>(&o);
 #pragma unroll
-    for (int c = 0; c < 8; ++c) t[c] = Elem<T>::from_f(rows::in_range<T>(v[c]));
-    return o;
+    for (int c = 0; c < 8; ++c) v[c] = rows::in_range<T>(v[c]);
+    return make_uint4(rows::two<T>(v[0], v[1]), rows::two<T>(v[2], v[3]), rows::two<T>(v[4], v[5]),
+                      rows::two<T>(v[6], v[7]));
 }
 
 template <typename T, int M, int N>

@@ -35,7 +35,7 @@ def test_embed_argument_checks(lib):
         return lib.lat_embed_wgrad(ids, w, n, dy, vocab, c, 1.0, -1, out, dt, ws, size, None, None)
 
     assert wgrad(ids=None) == wgrad(dy=None) == wgrad(out=None) == wgrad(w=1) == wgrad(c=20) == wgrad(dt=-1) == ARG
-    assert wgrad(dy=P(4104)) == wgrad(out=P(4104)) == ARG
+    assert wgrad(dy=P(4104)) == wgrad(out=P(4112)) == ARG
     need = lib.lat_embed_wgrad_ws_bytes(10, 100, 16)
     assert need > 0 and wgrad(size=need - 1) == wgrad(ws=None) == wgrad(ws=P(4104)) == WORKSPACE
     assert lib.lat_embed_wgrad_ws_bytes(-1, 100, 16) == lib.lat_embed_wgrad_ws_bytes(10, 0, 16) == 0
@@ -84,7 +84,7 @@ def test_norm_argument_checks(lib):
 
     assert bwd(dy=None) == bwd(h=None) == bwd(rstd=None) == bwd(dx=None) == bwd(c=12) == bwd(dt=4) == ARG
     assert bwd(h8=A, h8s=A) == bwd(h=None, h8=A) == ARG                            # both forms of h; no scales
-    assert bwd(dy=P(4104)) == bwd(dh=P(4104)) == bwd(dw=P(4104)) == bwd(dx=P(4104)) == ARG
+    assert bwd(dy=P(4104)) == bwd(dh=P(4104)) == bwd(dw=P(4098)) == bwd(dx=P(4104)) == ARG
     need = lib.lat_rms_norm_bwd_ws_bytes(10, 16)
     assert need > 0 and bwd(size=need - 1) == bwd(ws=None) == WORKSPACE
     assert bwd(n=0, dw=None) == 0                                                   # no rows, no dw
