@@ -372,24 +372,26 @@ __device__ __forceinline__ uint32_t path_rows(const Path &p, uint32_t step, int 
 }
 
 // A group's lanes read the tokens and rows of L steps at a time, one step each, and the next
-// ones before they add; kFlight rows of dy are in flight while kFlight are added.  A block
-// takes kThreads / L consecutive shares; if a token's run covers them all, their sums meet in
-// shared memory and the first share's head stands for the block.
+// ones before they add; kFlight rows of dy are in flight while kFlight are added.  A row of
+// more than 256 channels takes several groups (slabs), up to eight of them side by side in a
+// block, so that a block reads and writes long pieces.  A block takes `per_block` consecutive
+// shares; if a token's run covers them all, their sums meet in shared memory and the first
+// share's head stands for the block.
 template <typename T, int L>
-__global__ void __launch_bounds__(kThreads, 3) sums_kernel(Path p, const T *__restrict__ dy) {
+__global__ void __launch_bounds__(kThreads, 3) sums_kernel(Path p, const T *__restrict__ dy, int per_block) {
     pdl_enter();
-    constexpr int kGroups = kThreads / L;
     constexpr int kFlight = sizeof(T) == 4 || L == 4 ? 2 : 4;  // an even number of times per batch
     __shared__ float s_acc[8][kThreads];
     const int group = threadIdx.x / L, lane = threadIdx.x % L, first = (threadIdx.x & 31) / L * L;
     const uint32_t mask = (L == 32 ? 0xFFFFFFFFu : ((1u << (L & 31)) - 1u) << first);
-    const int v = blockIdx.x * kGroups + group;
+    const int slabs = L < 32 ? 1 : int(blockDim.x) / L / per_block;  // of a block
+    const int v = blockIdx.x * per_block + group / slabs;
     const uint32_t steps = p.vocab + p.n;
     const uint32_t s0 = uint32_t(min(uint64_t(v) * p.share, uint64_t(steps)));
     const uint32_t s1 = uint32_t(min(uint64_t(s0) + p.share, uint64_t(steps)));
     const uint32_t i0 = path_rows<L>(p, s0, lane, mask, first), i1 = path_rows<L>(p, s1, lane, mask, first);
     const uint32_t r0 = s0 - i0, r1 = s1 - i1;
-    const int vi = blockIdx.y * L + lane;
+    const int vi = (int(blockIdx.y) * slabs + group % slabs) * L + lane;
     const bool own = vi < p.c / 8;
     const uint32_t col = vi * 8;
     // the first token's run began in an earlier share; the last token's run goes on in the next one
@@ -458,14 +460,14 @@ __global__ void __launch_bounds__(kThreads, 3) sums_kernel(Path p, const T *__re
     }
     go_to(r1);
     const bool through = cut && goes_on && r == r0;  // the share lies inside one token's run
-    if (__syncthreads_and(through)) {
+    if (per_block > 1 && __syncthreads_and(through)) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) s_acc[e][threadIdx.x] = acc[e];
         __syncthreads();
-        if (group == 0 && own) {
-            for (int g = 1; g < kGroups; ++g)
+        if (group < slabs && own) {
+            for (int g = 1; g < per_block; ++g)
 #pragma unroll
-                for (int e = 0; e < 8; ++e) acc[e] += s_acc[e][g * L + lane];
+                for (int e = 0; e < 8; ++e) acc[e] += s_acc[e][g * slabs * L + threadIdx.x];
             rows::st(p.head + v * int64_t(p.c) + col, acc);
         }
     } else if (goes_on && own) {
@@ -624,15 +626,17 @@ lat_status wgrad(const I *ids, int64_t n, const T *dy, int64_t vocab, int c, flo
     Path p{w.key[at], w.row[at], uint32_t(n), uint32_t(vocab), 0, path_shares(n, vocab, c), c, scale, w.head, w.tail,
            w.open + 1, w.open, dtable};
     p.share = uint32_t((n + vocab + p.shares - 1) / p.shares);
+    const int groups = kThreads / lanes_of(c), slabs = (c / 8 + 31) / 32, side = std::min(slabs, groups);
+    const int per_block = groups / side;
     const lat_status st = by_lanes(c, [&](auto l) -> lat_status {
         constexpr int L = decltype(l)::value;
-        const dim3 grid(unsigned((p.shares + kThreads / L - 1) / (kThreads / L)), unsigned((c / 8 + L - 1) / L));
-        LAT_CUDA_TRY(launch_pdl(sums_kernel<T, L>, grid, dim3(kThreads), 0, s, p, dy));
+        const dim3 grid(unsigned((p.shares + per_block - 1) / per_block), unsigned((slabs + side - 1) / side));
+        LAT_CUDA_TRY(launch_pdl(sums_kernel<T, L>, grid, dim3(unsigned(L * side * per_block)), 0, s, p, dy, per_block));
         return LAT_OK;
     });
     if (st != LAT_OK || n == 0) return st;
     LAT_CUDA_TRY(launch_pdl(join_kernel, dim3(unsigned(std::min(p.shares, kJoinBlocks)), unsigned((c + 127) / 128)),
-                            dim3(32, kJoinRows), 0, s, p, kThreads / lanes_of(c)));
+                            dim3(32, kJoinRows), 0, s, p, per_block));
     return LAT_OK;
 }
 
