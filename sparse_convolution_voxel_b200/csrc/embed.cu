@@ -167,13 +167,13 @@ __device__ __forceinline__ uint32_t same_digit(uint32_t digit, int bits, bool in
 template <typename I, int R>
 __global__ void __launch_bounds__(kThreads) scatter_kernel(Pass p, Ids<I> d) {
     pdl_enter();
-    constexpr int kOwn = kMaxBins / kThreads;  // digits of a thread in the scan (at most)
-    __shared__ uint32_t s_cnt[kWarps][kMaxBins];
+    static_assert(kMaxBins == 4 * kThreads, "four digits per thread in the scan");
+    __shared__ uint4 s_cnt4[kWarps][kMaxBins / 4];
     __shared__ uint32_t s_scan[kWarps];
+    uint32_t(*s_cnt)[kMaxBins] = reinterpret_cast<uint32_t(*)[kMaxBins]>(s_cnt4);
     const int bins = 1 << p.bits, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int per = (bins + kThreads - 1) / kThreads, b0 = int(threadIdx.x) * per;
     const int64_t lo = (blockIdx.x * int64_t(kWarps) + warp) * (32 * R);
-    uint32_t key[R], rank[R], row[R], total[kOwn], start[kOwn];
+    uint32_t key[R], rank[R], row[R];
     int32_t bad = 0;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
@@ -181,24 +181,22 @@ __global__ void __launch_bounds__(kThreads) scatter_kernel(Pass p, Ids<I> d) {
         key[r] = i < p.n ? sort_key(p, d, i, bad) : 0u;
         row[r] = i < p.n ? (p.row_in ? p.row_in[i] : uint32_t(i)) : 0u;
     }
+    const bool own = int(threadIdx.x) * 4 < bins;  // this thread's digits 4 t .. 4 t + 3
+    uint4 total = make_uint4(0u, 0u, 0u, 0u), start = total;
+    if (own) {
+        total = reinterpret_cast<const uint4 *>(p.totals)[threadIdx.x];
+        start = reinterpret_cast<const uint4 *>(p.counts + int64_t(blockIdx.x) * bins)[threadIdx.x];
 #pragma unroll
-    for (int o = 0; o < kOwn; ++o) {
-        const bool own = o < per && b0 + o < bins;
-        total[o] = own ? p.totals[b0 + o] : 0u;
-        start[o] = own ? p.counts[int64_t(blockIdx.x) * bins + b0 + o] : 0u;
+        for (int w = 0; w < kWarps; ++w) s_cnt4[w][threadIdx.x] = make_uint4(0u, 0u, 0u, 0u);
     }
-    for (int b = threadIdx.x; b < bins; b += kThreads)
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) s_cnt[w][b] = 0;
-    // first position of each digit: an exclusive scan of the totals, a run of digits per thread
-    uint32_t sum = 0;
-#pragma unroll
-    for (int o = 0; o < kOwn; ++o) sum += total[o];
+    // first position of each digit: an exclusive scan of the totals
+    const uint32_t sum = total.x + total.y + total.z + total.w;
     const uint32_t upto = warp_scan(sum, lane);
     if (lane == 31) s_scan[warp] = upto;
     __syncthreads();
     uint32_t at = upto - sum;
-    for (int w = 0; w < warp; ++w) at += s_scan[w];
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) at += w < warp ? s_scan[w] : 0u;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
         const bool in = lo + r * 32 + lane < p.n;
@@ -211,16 +209,14 @@ __global__ void __launch_bounds__(kThreads) scatter_kernel(Pass p, Ids<I> d) {
         __syncwarp();
     }
     __syncthreads();
-#pragma unroll
-    for (int o = 0; o < kOwn; ++o) {
-        if (o >= per || b0 + o >= bins) break;
-        uint32_t run = at + start[o];
-        at += total[o];
+    if (own) {
+        uint4 run = make_uint4(at + start.x, at + total.x + start.y, at + total.x + total.y + start.z,
+                               at + total.x + total.y + total.z + start.w);
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
-            const uint32_t v = s_cnt[w][b0 + o];
-            s_cnt[w][b0 + o] = run;
-            run += v;
+            const uint4 v = s_cnt4[w][threadIdx.x];
+            s_cnt4[w][threadIdx.x] = run;
+            run = make_uint4(run.x + v.x, run.y + v.y, run.z + v.z, run.w + v.w);
         }
     }
     __syncthreads();
@@ -342,33 +338,51 @@ struct Path {
     int c;
     float scale;
     float *head, *tail;         // [shares][c]
-    int32_t *open, *open_count; // shares in which a run begins that goes on behind them, in any order
+    // shares in which a run begins that goes on behind them, in any order: the share, the token,
+    // the sorted rows up to the share's end
+    int4 *open;
+    int32_t *open_count;
     float *dtable;
 };
 
-// First index in [lo, hi) at which `before` no longer holds (hi if it holds everywhere).  W
-// lanes of a group (mask, first: its lanes in the warp) search together: each round splits
-// the range into W + 1 parts, so 500,000 rows take four dependent reads with 32 lanes.
-template <int W, typename F>
-__device__ __forceinline__ uint32_t first_not(uint32_t lo, uint32_t hi, int lane, uint32_t mask, int first, F &&before) {
-    while (lo < hi) {
-        const uint32_t span = hi - lo;
-        auto part = [&](uint32_t k) { return lo + uint32_t(uint64_t(span) * k / (W + 1)); };
-        // the probes are in order, so the votes are a prefix
-        const int k = __popc((__ballot_sync(mask, before(part(lane + 1))) & mask) >> first);
+// One range of a search: the first index in [lo, hi) at which `before` no longer holds (hi if it
+// holds everywhere).  W lanes of a group search together: a round splits the range into W + 1
+// parts, so 500,000 rows take four dependent reads with 32 lanes.
+template <int W>
+struct Range {
+    uint32_t lo, hi;
+    __device__ __forceinline__ uint32_t part(uint32_t k) const {
+        return lo + uint32_t(uint64_t(hi - lo) * k / (W + 1));
+    }
+    // votes of the group's lanes for their probes part(lane + 1): the probes are in order, so the votes are a prefix
+    __device__ __forceinline__ void narrow(uint32_t votes) {
+        if (lo >= hi) return;
+        const int k = __popc(votes);
         const uint32_t nlo = k == 0 ? lo : part(k) + 1, nhi = k == W ? hi : part(k + 1);
         lo = nlo;
         hi = nhi;
     }
-    return lo;
-}
+};
 
-// Sorted rows among the first `step` steps of the path: the first i with key[i] + i >= step
-// (key[i] + i increases strictly).
+// Sorted rows among the first a and the first b steps of the path: the first i with
+// key[i] + i >= a (b); key[i] + i increases strictly.  The two searches share their rounds.
+// mask, first: the group's lanes in its warp.
 template <int W>
-__device__ __forceinline__ uint32_t path_rows(const Path &p, uint32_t step, int lane, uint32_t mask, int first) {
-    return first_not<W>(step > p.vocab ? step - p.vocab : 0u, min(step, p.n), lane, mask, first,
-                        [&](uint32_t at) { return uint64_t(__ldg(p.key + at)) + at < step; });
+__device__ __forceinline__ void path_rows(const Path &p, uint32_t a, uint32_t b, int lane, uint32_t mask, int first,
+                                          uint32_t &ia, uint32_t &ib) {
+    Range<W> ra{a > p.vocab ? a - p.vocab : 0u, min(a, p.n)}, rb{b > p.vocab ? b - p.vocab : 0u, min(b, p.n)};
+    auto before = [&](const Range<W> &r, uint32_t step) {
+        if (r.lo >= r.hi) return false;
+        const uint32_t at = r.part(lane + 1);
+        return uint64_t(__ldg(p.key + at)) + at < step;
+    };
+    while (ra.lo < ra.hi || rb.lo < rb.hi) {
+        const bool ba = before(ra, a), bb = before(rb, b);
+        ra.narrow((__ballot_sync(mask, ba) & mask) >> first);
+        rb.narrow((__ballot_sync(mask, bb) & mask) >> first);
+    }
+    ia = ra.lo;
+    ib = rb.lo;
 }
 
 // A group's lanes read the tokens and rows of L steps at a time, one step each, and the next
@@ -389,7 +403,8 @@ __global__ void __launch_bounds__(kThreads, 3) sums_kernel(Path p, const T *__re
     const uint32_t steps = p.vocab + p.n;
     const uint32_t s0 = uint32_t(min(uint64_t(v) * p.share, uint64_t(steps)));
     const uint32_t s1 = uint32_t(min(uint64_t(s0) + p.share, uint64_t(steps)));
-    const uint32_t i0 = path_rows<L>(p, s0, lane, mask, first), i1 = path_rows<L>(p, s1, lane, mask, first);
+    uint32_t i0, i1;
+    path_rows<L>(p, s0, s1, lane, mask, first, i0, i1);
     const uint32_t r0 = s0 - i0, r1 = s1 - i1;
     const int vi = (int(blockIdx.y) * slabs + group % slabs) * L + lane;
     const bool own = vi < p.c / 8;
@@ -472,7 +487,7 @@ __global__ void __launch_bounds__(kThreads, 3) sums_kernel(Path p, const T *__re
         }
     } else if (goes_on && own) {
         rows::st((through ? p.head : p.tail) + v * int64_t(p.c) + col, acc);
-        if (!through && vi == 0) p.open[atomicAdd(p.open_count, 1)] = v;
+        if (!through && vi == 0) p.open[atomicAdd(p.open_count, 1)] = make_int4(v, int(r1), int(i1), 0);
     }
 }
 
@@ -485,21 +500,18 @@ constexpr int kJoinRows = 8, kJoinBlocks = 1184;
 __global__ void __launch_bounds__(32 * kJoinRows) join_kernel(Path p, int per_block) {
     pdl_enter();
     __shared__ int s_last;
-    __shared__ uint32_t s_row;
     __shared__ float4 s[kJoinRows][32];
     const int count = *p.open_count;
     for (int o = blockIdx.x; o < count; o += gridDim.x) {
-        const int v = p.open[o];
+        const int4 run = p.open[o];
+        const int v = run.x;
+        const uint32_t token = uint32_t(run.y);
         if (threadIdx.y == 0) {
-            const int lane = threadIdx.x;
-            const uint32_t s1 = (v + 1) * p.share, i1 = path_rows<32>(p, s1, lane, 0xFFFFFFFFu, 0), r = s1 - i1;
-            // the first sorted row past the run of token r
-            const uint32_t lo = first_not<32>(i1, p.n, lane, 0xFFFFFFFFu, 0,
-                                              [&](uint32_t at) { return __ldg(p.key + at) <= r; });
-            if (lane == 0) {
-                s_last = int((uint64_t(lo) + r) / p.share);  // the share of the step that stores the token
-                s_row = r;
-            }
+            // the first sorted row past the run
+            Range<32> r{uint32_t(run.z), p.n};
+            while (r.lo < r.hi)
+                r.narrow(__ballot_sync(0xFFFFFFFFu, __ldg(p.key + r.part(threadIdx.x + 1)) <= token));
+            if (threadIdx.x == 0) s_last = int((uint64_t(r.lo) + token) / p.share);  // the share that stores the token
         }
         __syncthreads();
         const int last = s_last;
@@ -529,7 +541,7 @@ __global__ void __launch_bounds__(32 * kJoinRows) join_kernel(Path p, int per_bl
         if (threadIdx.y == 0 && col < p.c) {
 #pragma unroll
             for (int q = 1; q < kJoinRows; ++q) add(s[q][threadIdx.x]);
-            *reinterpret_cast<float4 *>(p.dtable + int64_t(s_row) * p.c + col) =
+            *reinterpret_cast<float4 *>(p.dtable + int64_t(token) * p.c + col) =
                 make_float4(acc.x * p.scale, acc.y * p.scale, acc.z * p.scale, acc.w * p.scale);
         }
         __syncthreads();
@@ -568,7 +580,7 @@ static int key_bits(int64_t vocab) {
 
 // Rows per thread of the sort's tiles: small tiles while there are few rows, so that enough
 // SMs sort; large ones later, so that the counts stay few.
-static int tile_rounds(int64_t n) { return n <= 65536 ? 2 : 8; }
+static int tile_rounds(int64_t n) { return n <= 65536 ? 2 : 4; }
 static int64_t tiles_of(int64_t n) {
     const int64_t tile = kThreads * tile_rounds(n);
     return (n + tile - 1) / tile;
@@ -577,7 +589,8 @@ static int64_t tiles_of(int64_t n) {
 struct Ws {
     uint32_t *key[2], *row[2], *counts, *totals;
     float *head, *tail;
-    int32_t *open;  // the count, then the list
+    int4 *open;
+    int32_t *open_count;
     size_t bytes;
     Ws(void *base, int64_t n, int64_t vocab, int c) {
         Carver cv(base);
@@ -590,7 +603,8 @@ struct Ws {
         const size_t part = size_t(path_shares(n, vocab, c)) * size_t(c);
         head = cv.take<float>(part);
         tail = cv.take<float>(part);
-        open = cv.take<int32_t>(size_t(path_shares(n, vocab, c)) + 1);
+        open = cv.take<int4>(size_t(path_shares(n, vocab, c)));
+        open_count = cv.take<int32_t>(1);
         bytes = align_up(cv.used, 256);
     }
 };
@@ -604,13 +618,13 @@ lat_status wgrad(const I *ids, int64_t n, const T *dy, int64_t vocab, int c, flo
         auto kern = sort_small_kernel<I>;
         LAT_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kSmallSmem)));
         LAT_CUDA_TRY(launch_pdl(kern, dim3(1), dim3(kSmallThreads), kSmallSmem, s, Ids<I>{ids, vocab, pad}, int(n),
-                                key_bits(vocab), w.key[0], w.row[0], w.open, d_status));
+                                key_bits(vocab), w.key[0], w.row[0], w.open_count, d_status));
     } else if (n > 0) {
-        const int bits = key_bits(vocab), passes = (bits + kMaxBits - 1) / kMaxBits, digit = (bits + passes - 1) / passes;
+        const int bits = key_bits(vocab), passes = (bits + kMaxBits - 1) / kMaxBits, digit = std::max(2, (bits + passes - 1) / passes);
         const int tiles = int(tiles_of(n)), bins = 1 << digit;
         const bool few = tile_rounds(n) == 2;
-        auto count = few ? count_kernel<I, 2> : count_kernel<I, 8>;
-        auto scatter = few ? scatter_kernel<I, 2> : scatter_kernel<I, 8>;
+        auto count = few ? count_kernel<I, 2> : count_kernel<I, 4>;
+        auto scatter = few ? scatter_kernel<I, 2> : scatter_kernel<I, 4>;
         const Ids<I> d{ids, vocab, pad};
         for (int i = 0; i < passes; ++i) {
             const int to = i & 1;
@@ -618,13 +632,13 @@ lat_status wgrad(const I *ids, int64_t n, const T *dy, int64_t vocab, int c, flo
                    tiles, i * digit, digit};
             LAT_CUDA_TRY(launch_pdl(count, dim3(tiles), dim3(kThreads), 0, s, p, d, i ? nullptr : d_status));
             LAT_CUDA_TRY(launch_pdl(tile_scan_kernel, dim3((bins + 31) / 32), dim3(32, 32), 0, s, w.counts, w.totals,
-                                    tiles, bins, w.open));
+                                    tiles, bins, w.open_count));
             LAT_CUDA_TRY(launch_pdl(scatter, dim3(tiles), dim3(kThreads), 0, s, p, d));
             at = to;
         }
     }
     Path p{w.key[at], w.row[at], uint32_t(n), uint32_t(vocab), 0, path_shares(n, vocab, c), c, scale, w.head, w.tail,
-           w.open + 1, w.open, dtable};
+           w.open, w.open_count, dtable};
     p.share = uint32_t((n + vocab + p.shares - 1) / p.shares);
     const int groups = kThreads / lanes_of(c), slabs = (c / 8 + 31) / 32, side = std::min(slabs, groups);
     const int per_block = groups / side;
@@ -635,7 +649,8 @@ lat_status wgrad(const I *ids, int64_t n, const T *dy, int64_t vocab, int c, flo
         return LAT_OK;
     });
     if (st != LAT_OK || n == 0) return st;
-    LAT_CUDA_TRY(launch_pdl(join_kernel, dim3(unsigned(std::min(p.shares, kJoinBlocks)), unsigned((c + 127) / 128)),
+    const int cols = (c + 127) / 128;
+    LAT_CUDA_TRY(launch_pdl(join_kernel, dim3(unsigned(std::min(p.shares, std::max(1, kJoinBlocks / cols))), unsigned(cols)),
                             dim3(32, kJoinRows), 0, s, p, per_block));
     return LAT_OK;
 }
