@@ -8,10 +8,16 @@
 // Everything between the loads and the one rounding of each output is fp32.  Both passes
 // read each input once and write each output once; what bounds them is memory.
 //
-// A row lies in the registers of its lanes, 8 channels (16 bytes of fp16 / bf16) each:
-// up to 256 channels a group of 4 to 32 lanes takes a row (K = 1), up to 512 a warp
-// (K = 2 slices per lane), wider rows a block of as many warps as the row needs
-// (K = 1 up to 4096 channels, else 2), whose sums meet in shared memory once per row.
+// A row lies in the registers of its lanes, 8 channels each: up to 256 channels a group of 4
+// to 32 lanes takes a row (K = 1 slice per lane), up to 512 a warp (K = 2), wider rows a
+// block with K = 1 (to 1024 channels), 2 (to 8192) or 4 slices per lane, whose sums meet in
+// shared memory once per row.
+//
+// The backward pass walks several rows per group.  A lane copies its slices of the rows ahead
+// with cp.async into a ring of its own in shared memory -- it alone reads them, so its own
+// copies are all it waits for -- which keeps some 150 KB per SM in flight without the
+// registers that loads ahead would take (500k x 128 bf16 from 8-bit rows, 450 MB: 98 us with
+// a row's loads in front of its work, 106 us with the next row in registers, 89 us so).
 //
 // dw: a fixed number of blocks (never more than there are row groups) walks the rows in
 // fixed steps with the sums of its rows in registers, adds its groups' sums in order in
@@ -20,6 +26,7 @@
 #include <algorithm>
 
 #include "rows.cuh"
+#include "tc_ptx.cuh"
 
 namespace lat {
 namespace norm {
@@ -27,8 +34,8 @@ namespace norm {
 using rows::Slice8;
 
 constexpr int kThreads = 256;      // of the kernels that take several rows per block
-constexpr int kShares = 592;       // blocks of the backward pass: four per B200 SM
-constexpr int kMaxWarps = 32;
+constexpr int kWideThreads = 512;  // at most, where a block takes a row
+constexpr int kMaxWarps = kWideThreads / 32;
 
 // Sum over the L lanes of a row's group (L <= 32), or over the block (L == 0).
 template <int L>
@@ -61,14 +68,14 @@ template <typename T> struct Fwd {
 };
 
 template <typename T, int L, int K>
-__global__ void __launch_bounds__(L == 0 ? 1024 : kThreads) norm_fwd_kernel(Fwd<T> a) {
+__global__ void __launch_bounds__(L == 0 ? kWideThreads : kThreads) norm_fwd_kernel(Fwd<T> a) {
     pdl_enter();
     __shared__ float s_sum[2 * kMaxWarps];
     const int lanes = L == 0 ? int(blockDim.x) : L;
     const int64_t row = L == 0 ? int64_t(blockIdx.x) : blockIdx.x * int64_t(kThreads / (L == 0 ? 1 : L)) + threadIdx.x / lanes;
     const int lane = L == 0 ? int(threadIdx.x) : int(threadIdx.x) % lanes;
     const int slices = a.c / 8;
-    Slice8<T> xs[K], rs[K], ws[K];
+    Slice8<T> xs[K], rs[K];
     bool in[K];
 #pragma unroll
     for (int k = 0; k < K; ++k) {
@@ -77,7 +84,6 @@ __global__ void __launch_bounds__(L == 0 ? 1024 : kThreads) norm_fwd_kernel(Fwd<
         const int64_t at = row * a.c + vi * 8;
         xs[k] = in[k] ? rows::ld(a.x + at) : rows::zero_slice<T>();
         if (a.res) rs[k] = in[k] ? rows::ld(a.res + at) : rows::zero_slice<T>();
-        if (a.w) ws[k] = vi < slices ? rows::ld(a.w + vi * 8) : rows::zero_slice<T>();
     }
     float v[K][8];
     float ss = 0.f;
@@ -105,7 +111,7 @@ __global__ void __launch_bounds__(L == 0 ? 1024 : kThreads) norm_fwd_kernel(Fwd<
         if (a.h8) rows::q8_store(v[k], in[k], a.h8, a.h8s, row, a.c, vi);
         if (a.w) {
             float w[8];
-            rows::to_f(ws[k], w);
+            rows::to_f(vi < slices ? rows::ld(a.w + vi * 8) : rows::zero_slice<T>(), w);
 #pragma unroll
             for (int e = 0; e < 8; ++e) v[k][e] = v[k][e] * rstd * w[e];
         } else {
@@ -127,90 +133,192 @@ template <typename T> struct Bwd {
     int c;
 };
 
+// Rows in the ring (the one at work included): what 200 KB of shared memory per SM admit.
+template <typename T, int L, int K>
+constexpr int ring_rows() {
+    return K == 4 ? (sizeof(T) == 4 ? 1 : 2) : sizeof(T) == 4 ? 2 : K == 2 && L == 0 ? 3 : 4;
+}
+// Bytes of a thread's slices of one row.
+template <typename T, int K, bool Q8>
+constexpr int ring_bytes(bool dh) {
+    return K * (int(8 * sizeof(T)) * (1 + (Q8 ? 0 : 1) + (dh ? 1 : 0)) + (Q8 ? 8 : 0));
+}
+
 template <typename T, int L, int K, bool Q8>
-__global__ void __launch_bounds__(L == 0 ? 1024 : kThreads) norm_bwd_kernel(Bwd<T> a) {
+__global__ void __launch_bounds__(L == 0 ? kWideThreads : kThreads, L > 0 && K == 1 ? 4 : 1) norm_bwd_kernel(Bwd<T> a) {
     pdl_enter();
     __shared__ float s_sum[2 * kMaxWarps];
-    extern __shared__ float s_dw[];  // L > 0: [kThreads / L][c], the groups' sums
+    extern __shared__ __align__(16) uint8_t s_ring[];  // and, at the end, the groups' sums of dw: [kThreads / L][c]
     constexpr int G = L == 0 ? 1 : kThreads / (L == 0 ? 1 : L);  // rows the block takes at a time
+    constexpr int D = ring_rows<T, L, K>(), CH = int(sizeof(T)) / 2;  // 16-byte chunks per slice
+    const int threads = L == 0 ? int(blockDim.x) : kThreads;
     const int lanes = L == 0 ? int(blockDim.x) : L;
     const int group = L == 0 ? 0 : int(threadIdx.x) / lanes;
     const int lane = L == 0 ? int(threadIdx.x) : int(threadIdx.x) % lanes;
     const int slices = a.c / 8;
-    float w[K][8], dw[K][8];
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-        const int vi = lane + k * lanes;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            w[k][e] = 1.f;
-            dw[k][e] = 0.f;
-        }
-        if (a.w && vi < slices) rows::to_f(rows::ld(a.w + vi * 8), w[k]);
-    }
-    const float inv_c = 1.f / float(a.c);
-    int turn = 0;
-    for (int64_t row0 = blockIdx.x * int64_t(G); row0 < a.n; row0 += gridDim.x * int64_t(G)) {
-        const int64_t row = row0 + group;
-        const float rstd = row < a.n ? __ldg(a.rstd + row) : 0.f;
-        Slice8<T> ds[K], hs[K], ps[K];
-        uint2 hb[K];
-        int he[K];
-        bool in[K];
+    const bool with_dh = a.dh != nullptr;
+    // a row of the ring: 16-byte chunks of dy, h (or 8-byte chunks of h8, last) and dh, each one
+    // chunk after the other for all threads
+    const int row_bytes = ring_bytes<T, K, Q8>(with_dh) * threads;
+    auto chunk = [&](int slot, int array, int k, int half) {
+        return s_ring + slot * row_bytes + ((array * K + k) * CH + half) * threads * 16 + int(threadIdx.x) * 16;
+    };
+    const int dh_at = Q8 ? 1 : 2, h8_at = 1 + (with_dh ? 1 : 0);
+    auto chunk8 = [&](int slot, int k) {
+        return s_ring + slot * row_bytes + h8_at * K * CH * threads * 16 + (k * threads + int(threadIdx.x)) * 8;
+    };
+    auto copy = [&](int64_t row, int slot) {
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             const int vi = lane + k * lanes;
-            in[k] = row < a.n && vi < slices;
+            if (row >= a.n || vi >= slices) continue;
             const int64_t at = row * a.c + vi * 8;
-            ds[k] = in[k] ? rows::ld(a.dy + at) : rows::zero_slice<T>();
-            if constexpr (Q8) {
-                hb[k] = make_uint2(0u, 0u);
-                he[k] = 1;
-                if (in[k]) rows::q8_load(a.h8, a.h8s, row, a.c, vi, hb[k], he[k]);
-            } else {
-                hs[k] = in[k] ? rows::ld(a.h + at) : rows::zero_slice<T>();
+#pragma unroll
+            for (int half = 0; half < CH; ++half) {
+                ptx::cp_async16(chunk(slot, 0, k, half), a.dy + at + half * 4, 16u);
+                if constexpr (!Q8) ptx::cp_async16(chunk(slot, 1, k, half), a.h + at + half * 4, 16u);
+                if (with_dh) ptx::cp_async16(chunk(slot, dh_at, k, half), a.dh + at + half * 4, 16u);
             }
-            if (a.dh) ps[k] = in[k] ? rows::ld(a.dh + at) : rows::zero_slice<T>();
+            if constexpr (Q8) ptx::cp_async8(chunk8(slot, k), a.h8 + at);
         }
-        float xh[K][8], g[K][8];
-        float sum = 0.f;
+        ptx::cp_async_commit();
+    };
+    auto slice = [&](int slot, int array, int k) {
+        Slice8<T> r;
 #pragma unroll
-        for (int k = 0; k < K; ++k) {
-            rows::to_f(ds[k], g[k]);
-            if constexpr (Q8) rows::q8_to_f(hb[k], he[k], xh[k]);
-            else rows::to_f(hs[k], xh[k]);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                xh[k][e] *= rstd;
-                dw[k][e] = fmaf(g[k][e], xh[k][e], dw[k][e]);
-                g[k][e] *= w[k][e];
-                sum = fmaf(g[k][e], xh[k][e], sum);
-            }
+        for (int half = 0; half < CH; ++half) {
+            const uint4 q = *reinterpret_cast<const uint4 *>(chunk(slot, array, k, half));
+            r.v[4 * half] = q.x;
+            r.v[4 * half + 1] = q.y;
+            r.v[4 * half + 2] = q.z;
+            r.v[4 * half + 3] = q.w;
         }
-        const float mean = row_sum<L>(sum, s_sum, turn) * inv_c;
+        return r;
+    };
+    using rows::add2;
+    using rows::both;
+    using rows::fma2;
+    using rows::mul2;
+    float2 dw[K][4] = {};
+    // one slice per lane: a row's g and h stay in registers; more: they are computed again, which
+    // leaves room for two blocks per SM.  The weights stay but for four slices (from L1 then).
+    constexpr bool kKeep = K == 1, kKeepW = K < 4;
+    float2 ws[kKeepW ? K : 1][4];
+    auto weight = [&](int k, float2 (&v)[4]) {
+        const int vi = lane + k * lanes;
+        if (a.w && vi < slices) {
+            rows::to_f2(rows::ld(a.w + vi * 8), v);
+        } else {
 #pragma unroll
-        for (int k = 0; k < K; ++k) {
-            if (!in[k]) continue;
-            float p[8] = {};
-            if (a.dh) rows::to_f(ps[k], p);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) p[e] = fmaf(rstd, g[k][e] - xh[k][e] * mean, p[e]);
-            rows::st(a.dx + row * a.c + (lane + k * lanes) * 8, p);
+            for (int e = 0; e < 4; ++e) v[e] = both(1.f);
         }
+    };
+    if constexpr (kKeepW) {
+#pragma unroll
+        for (int k = 0; k < K; ++k) weight(k, ws[k]);
     }
+    const float inv_c = 1.f / float(a.c);
+    const int64_t stride = gridDim.x * int64_t(G);
+    struct Small {  // the row's rstd and scale bytes, read one row ahead
+        float rstd;
+        int e[K];
+    };
+    auto small = [&](int64_t row) {
+        Small r;
+        r.rstd = row < a.n ? __ldg(a.rstd + row) : 0.f;
+        if constexpr (Q8) {
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                const int vi = lane + k * lanes;
+                r.e[k] = row < a.n && vi < slices ? __ldg(a.h8s + row * rows::q8_groups(a.c) + (vi >> 2)) : 1;
+            }
+        }
+        return r;
+    };
+    int slot = 0, ahead = D - 1;
+    // slice k of d = rstd dy, of h, and of g = rstd dy w
+    auto terms = [&](const Small &m, int k, float2 (&d)[4], float2 (&h)[4], float2 (&g)[4]) {
+        rows::to_f2(slice(slot, 0, k), d);
+        if constexpr (Q8) rows::q8_to_f2(*reinterpret_cast<const uint2 *>(chunk8(slot, k)), m.e[k], h);
+        else rows::to_f2(slice(slot, 1, k), h);
+        float2 w[4];
+        if constexpr (!kKeepW) weight(k, w);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            d[e] = mul2(d[e], both(m.rstd));
+            g[e] = mul2(d[e], kKeepW ? ws[k][e] : w[e]);
+        }
+    };
+    int turn = 0;
+    const int64_t first = blockIdx.x * int64_t(G);
+#pragma unroll
+    for (int d = 0; d < D - 1; ++d) copy(first + d * stride + group, d);
+    Small cur = small(first + group);
+    for (int64_t row0 = first; row0 < a.n; row0 += stride) {
+        const int64_t row = row0 + group;
+        copy(row + (D - 1) * stride, ahead);
+        const Small next = small(row + stride);
+        ptx::cp_async_wait<D - 1>();
+        float2 sum = both(0.f), h[kKeep ? K : 1][4], g[kKeep ? K : 1][4];
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            if (row >= a.n || lane + k * lanes >= slices) continue;
+            constexpr int S = kKeep ? 1 : 0;
+            float2 d[4];
+            terms(cur, k, d, h[S * k], g[S * k]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                dw[k][e] = fma2(d[e], h[S * k][e], dw[k][e]);
+                sum = fma2(g[S * k][e], h[S * k][e], sum);
+            }
+        }
+        // dx = g - h rstd^2 mean(g h) + dh
+        const float at = row_sum<L>(sum.x + sum.y, s_sum, turn) * inv_c * cur.rstd * cur.rstd;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            if (row >= a.n || lane + k * lanes >= slices) continue;
+            constexpr int S = kKeep ? 1 : 0;
+            float2 d[4];
+            if constexpr (!kKeep) terms(cur, k, d, h[0], g[0]);
+            if (with_dh) {
+                float2 p[4];
+                rows::to_f2(slice(slot, dh_at, k), p);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) g[S * k][e] = add2(g[S * k][e], p[e]);
+            }
+            float out[8];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float2 o = fma2(h[S * k][e], both(-at), g[S * k][e]);
+                out[2 * e] = o.x;
+                out[2 * e + 1] = o.y;
+            }
+            rows::st(a.dx + row * a.c + (lane + k * lanes) * 8, out);
+        }
+        cur = next;
+        slot = slot + 1 == D ? 0 : slot + 1;
+        ahead = ahead + 1 == D ? 0 : ahead + 1;
+    }
+    ptx::cp_async_wait<0>();
     if (!a.partial) return;
     float *out = a.partial + blockIdx.x * int64_t(a.c);
     if constexpr (L == 0) {
 #pragma unroll
         for (int k = 0; k < K; ++k)
-            if (lane + k * lanes < slices) rows::st(out + (lane + k * lanes) * 8, dw[k]);
+            if (lane + k * lanes < slices) {
+                const float v[8] = {dw[k][0].x, dw[k][0].y, dw[k][1].x, dw[k][1].y,
+                                    dw[k][2].x, dw[k][2].y, dw[k][3].x, dw[k][3].y};
+                rows::st(out + (lane + k * lanes) * 8, v);
+            }
     } else {
+        float *s_dw = reinterpret_cast<float *>(s_ring);
+        __syncthreads();
 #pragma unroll
         for (int k = 0; k < K; ++k)
             if (lane + k * lanes < slices) {
                 float4 *d = reinterpret_cast<float4 *>(s_dw + group * a.c + (lane + k * lanes) * 8);
-                d[0] = make_float4(dw[k][0], dw[k][1], dw[k][2], dw[k][3]);
-                d[1] = make_float4(dw[k][4], dw[k][5], dw[k][6], dw[k][7]);
+                d[0] = make_float4(dw[k][0].x, dw[k][0].y, dw[k][1].x, dw[k][1].y);
+                d[1] = make_float4(dw[k][2].x, dw[k][2].y, dw[k][3].x, dw[k][3].y);
             }
         __syncthreads();
         for (int c = threadIdx.x; c < a.c; c += kThreads) {
@@ -248,14 +356,16 @@ __global__ void __launch_bounds__(1024) norm_dw_kernel(const float *__restrict__
 template <typename F>
 static lat_status by_layout(int c, F &&f) {
     const int slices = c / 8;
-    if (slices <= 4) return f(std::integral_constant<int, 4>{}, std::integral_constant<int, 1>{}, kThreads);
-    if (slices <= 8) return f(std::integral_constant<int, 8>{}, std::integral_constant<int, 1>{}, kThreads);
-    if (slices <= 16) return f(std::integral_constant<int, 16>{}, std::integral_constant<int, 1>{}, kThreads);
-    if (slices <= 32) return f(std::integral_constant<int, 32>{}, std::integral_constant<int, 1>{}, kThreads);
-    if (slices <= 64) return f(std::integral_constant<int, 32>{}, std::integral_constant<int, 2>{}, kThreads);
-    if (slices <= 512)
-        return f(std::integral_constant<int, 0>{}, std::integral_constant<int, 1>{}, (slices + 31) / 32 * 32);
-    return f(std::integral_constant<int, 0>{}, std::integral_constant<int, 2>{}, (slices + 63) / 64 * 32);
+    auto threads = [&](int k) { return (slices + 32 * k - 1) / (32 * k) * 32; };
+    using std::integral_constant;
+    if (slices <= 4) return f(integral_constant<int, 4>{}, integral_constant<int, 1>{}, kThreads);
+    if (slices <= 8) return f(integral_constant<int, 8>{}, integral_constant<int, 1>{}, kThreads);
+    if (slices <= 16) return f(integral_constant<int, 16>{}, integral_constant<int, 1>{}, kThreads);
+    if (slices <= 32) return f(integral_constant<int, 32>{}, integral_constant<int, 1>{}, kThreads);
+    if (slices <= 64) return f(integral_constant<int, 32>{}, integral_constant<int, 2>{}, kThreads);
+    if (slices <= 128) return f(integral_constant<int, 0>{}, integral_constant<int, 1>{}, threads(1));
+    if (slices <= 1024) return f(integral_constant<int, 0>{}, integral_constant<int, 2>{}, threads(2));
+    return f(integral_constant<int, 0>{}, integral_constant<int, 4>{}, threads(4));
 }
 
 // Rows a block takes at a time.
@@ -266,9 +376,10 @@ static int rows_per_block(int c) {
     return slices <= 64 ? kThreads / l : 1;
 }
 
+// Blocks of the backward pass: as many as fit a B200's 148 SMs at once, by the ring.
 static int64_t shares(int64_t n, int c) {
-    const int per = rows_per_block(c);
-    return std::max<int64_t>(1, std::min<int64_t>(kShares, (n + per - 1) / per));
+    const int64_t per = rows_per_block(c), most = c <= 256 ? 592 : c <= 512 ? 296 : c <= 1024 ? 592 : c <= 8192 ? 296 : 148;
+    return std::max<int64_t>(1, std::min<int64_t>(most, (n + per - 1) / per));
 }
 
 template <typename T>
@@ -294,12 +405,15 @@ lat_status bwd(const void *dy, const void *dh, const void *h, const void *h8, co
     const int64_t blocks = shares(n, c);
     const lat_status st = by_layout(c, [&](auto l, auto k, int threads) -> lat_status {
         constexpr int L = decltype(l)::value, K = decltype(k)::value;
-        const size_t smem = L == 0 ? 0 : sizeof(float) * size_t(kThreads / (L == 0 ? 1 : L)) * size_t(c);
-        if (h8)
-            LAT_CUDA_TRY(launch_pdl(norm_bwd_kernel<T, L, K, true>, dim3(unsigned(blocks)), dim3(threads), smem, s, a));
-        else
-            LAT_CUDA_TRY(launch_pdl(norm_bwd_kernel<T, L, K, false>, dim3(unsigned(blocks)), dim3(threads), smem, s, a));
-        return LAT_OK;
+        auto go = [&](auto kern, size_t row_bytes) -> lat_status {
+            const size_t sums = L == 0 ? 0 : sizeof(float) * size_t(kThreads / (L == 0 ? 1 : L)) * size_t(c);
+            const size_t smem = std::max(sums, row_bytes * size_t(threads) * ring_rows<T, L, K>());
+            LAT_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)));
+            LAT_CUDA_TRY(launch_pdl(kern, dim3(unsigned(blocks)), dim3(threads), smem, s, a));
+            return LAT_OK;
+        };
+        return h8 ? go(norm_bwd_kernel<T, L, K, true>, ring_bytes<T, K, true>(dh != nullptr))
+                  : go(norm_bwd_kernel<T, L, K, false>, ring_bytes<T, K, false>(dh != nullptr));
     });
     if (st != LAT_OK || !dw) return st;
     LAT_CUDA_TRY(launch_pdl(norm_dw_kernel, dim3(unsigned((c + 31) / 32)), dim3(32, 32), 0, s, partial, int(blocks), c,

@@ -2,9 +2,11 @@
 // power-of-two scale per 32 channels, and back.  The format is in rows.cuh.
 //
 // Both are one pass over the rows, bound by memory: pack moves (e + 33/32) bytes per
-// value, unpack the same.  A lane takes 8 channels, the four lanes of a group exchange
-// their largest magnitudes by shuffles.  L lanes take a row (a power of two, 4 to 32);
-// wider rows are taken by a warp in steps of 32 slices.
+// value, unpack the same.  Rows of whole groups (c a multiple of 32) are one run of
+// groups: a lane takes 16 channels, 16 bytes of e4m3 and 32 (fp16 / bf16) or 2 x 32 (fp32)
+// of values, and two lanes make a group.  Other rows: a lane takes 8 channels, the four
+// lanes of a group exchange their largest magnitudes, L lanes take a row (a power of two, 4
+// to 32) and a warp takes wider rows in steps of 32 slices.
 #include "rows.cuh"
 
 namespace lat {
@@ -45,6 +47,45 @@ unpack_kernel(const uint8_t *__restrict__ q, const uint8_t *__restrict__ scale, 
     }
 }
 
+// Whole groups: thread t takes channels 16 t .. 16 t + 15 of the run of n * c.
+template <typename T>
+__global__ void __launch_bounds__(kThreads)
+pack_run_kernel(const T *__restrict__ x, int64_t halves, uint8_t *__restrict__ q, uint8_t *__restrict__ scale) {
+    pdl_enter();
+    const int64_t t = blockIdx.x * int64_t(kThreads) + threadIdx.x;
+    const bool in = t < halves;
+    float v[2][8] = {};
+    if (in) rows::ld16(x + t * 16, v);
+    float m = fmaxf(rows::finite_amax(v[0]), rows::finite_amax(v[1]));
+    m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+    if (!in) return;
+    const int e = rows::q8_exponent(m);
+    const uint2 a = rows::q8_from_f(v[0], e), b = rows::q8_from_f(v[1], e);
+    reinterpret_cast<uint4 *>(q)[t] = make_uint4(a.x, a.y, b.x, b.y);
+    if ((t & 1) == 0) scale[t >> 1] = uint8_t(e);
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads)
+unpack_run_kernel(const uint8_t *__restrict__ q, const uint8_t *__restrict__ scale, int64_t halves, T *__restrict__ x) {
+    pdl_enter();
+    const int64_t t = blockIdx.x * int64_t(kThreads) + threadIdx.x;
+    if (t >= halves) return;
+    const uint4 r = __ldg(reinterpret_cast<const uint4 *>(q) + t);
+    const int e = __ldg(scale + (t >> 1));
+    float v[2][8];
+    rows::q8_to_f(make_uint2(r.x, r.y), e, v[0]);
+    rows::q8_to_f(make_uint2(r.z, r.w), e, v[1]);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        v[0][i] = rows::in_range<T>(v[0][i]);
+        v[1][i] = rows::in_range<T>(v[1][i]);
+    }
+    rows::st16(x + t * 16, v);
+}
+
+static unsigned run_blocks(int64_t halves) { return unsigned((halves + kThreads - 1) / kThreads); }
+
 template <typename F>
 static lat_status by_lanes(int c, F &&f) {
     const int slices = c / 8;
@@ -56,6 +97,11 @@ static lat_status by_lanes(int c, F &&f) {
 
 template <typename T>
 lat_status pack(const void *x, int64_t n, int c, uint8_t *q, uint8_t *scale, cudaStream_t s) {
+    if (c % rows::kQ8Group == 0 && rows::aligned(x, 32)) {
+        LAT_CUDA_TRY(launch_pdl(pack_run_kernel<T>, dim3(run_blocks(n * c / 16)), dim3(kThreads), 0, s,
+                                static_cast<const T *>(x), n * c / 16, q, scale));
+        return LAT_OK;
+    }
     return by_lanes(c, [&](auto l) -> lat_status {
         constexpr int L = decltype(l)::value;
         const int64_t per = kThreads / L;
@@ -67,6 +113,11 @@ lat_status pack(const void *x, int64_t n, int c, uint8_t *q, uint8_t *scale, cud
 
 template <typename T>
 lat_status unpack(const uint8_t *q, const uint8_t *scale, int64_t n, int c, void *x, cudaStream_t s) {
+    if (c % rows::kQ8Group == 0 && rows::aligned(x, 32)) {
+        LAT_CUDA_TRY(launch_pdl(unpack_run_kernel<T>, dim3(run_blocks(n * c / 16)), dim3(kThreads), 0, s, q, scale,
+                                n * c / 16, static_cast<T *>(x)));
+        return LAT_OK;
+    }
     return by_lanes(c, [&](auto l) -> lat_status {
         constexpr int L = decltype(l)::value;
         const int64_t per = kThreads / L;

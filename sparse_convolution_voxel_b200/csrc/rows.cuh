@@ -95,6 +95,62 @@ __device__ __forceinline__ void st(T *p, const float (&v)[8]) {
         *reinterpret_cast<uint4 *>(p) = make_uint4(s.v[0], s.v[1], s.v[2], s.v[3]);
 }
 
+// 16 channels at a 32-byte aligned address: one 256-bit access (fp16 / bf16) or two (fp32).
+__device__ __forceinline__ Slice8<float> ld32(const void *p) { return ld(static_cast<const float *>(p)); }
+template <typename T>
+__device__ __forceinline__ void ld16(const T *p, float (&v)[2][8]) {
+    if constexpr (sizeof(T) == 4) {
+        to_f(ld(p), v[0]);
+        to_f(ld(p + 8), v[1]);
+    } else {
+        const Slice8<float> r = ld32(p);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            Slice8<T> s;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) s.v[c] = r.v[4 * h + c];
+            to_f(s, v[h]);
+        }
+    }
+}
+template <typename T>
+__device__ __forceinline__ void st16(T *p, const float (&v)[2][8]) {
+    if constexpr (sizeof(T) == 4) {
+        st(p, v[0]);
+        st(p + 8, v[1]);
+    } else {
+        float w[8];
+#pragma unroll
+        for (int c = 0; c < 8; ++c) w[c] = __uint_as_float(two<T>(v[c / 4][2 * (c % 4)], v[c / 4][2 * (c % 4) + 1]));
+        st(reinterpret_cast<float *>(p), w);
+    }
+}
+
+// Two fp32 operations in one instruction (sm_100).
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;"
+        : "=l"(r)
+        : "l"(*reinterpret_cast<uint64_t *>(&a)), "l"(*reinterpret_cast<uint64_t *>(&b)),
+          "l"(*reinterpret_cast<uint64_t *>(&c)));
+    return *reinterpret_cast<float2 *>(&r);
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;"
+        : "=l"(r)
+        : "l"(*reinterpret_cast<uint64_t *>(&a)), "l"(*reinterpret_cast<uint64_t *>(&b)));
+    return *reinterpret_cast<float2 *>(&r);
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;"
+        : "=l"(r)
+        : "l"(*reinterpret_cast<uint64_t *>(&a)), "l"(*reinterpret_cast<uint64_t *>(&b)));
+    return *reinterpret_cast<float2 *>(&r);
+}
+__device__ __forceinline__ float2 both(float a) { return make_float2(a, a); }
+
 // ------------------------------------------------------------------- 8-bit rows
 // A group of 32 channels of one row shares the scale 2^(E - 127), E >= 1 the smallest
 // exponent byte with amax <= 448 * scale (448: the largest e4m3 value), amax over the
@@ -137,18 +193,30 @@ __device__ __forceinline__ uint2 q8_from_f(const float (&v)[8], int e) {
     return make_uint2(q8_pair(u[0], u[1]) | (q8_pair(u[2], u[3]) << 16),
                       q8_pair(u[4], u[5]) | (q8_pair(u[6], u[7]) << 16));
 }
-__device__ __forceinline__ void q8_two(uint32_t w, float s, float &a, float &b) {
-    const __half2_raw r = __nv_cvt_fp8x2_to_halfraw2(__nv_fp8x2_storage_t(w & 0xFFFFu), __NV_E4M3);
-    const float2 f = __half22float2(__half2(r));
-    a = f.x * s;
-    b = f.y * s;
+template <typename T>
+__device__ __forceinline__ void to_f2(const Slice8<T> &s, float2 (&v)[4]) {
+    float f[8];
+    to_f(s, f);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = make_float2(f[2 * e], f[2 * e + 1]);
 }
+__device__ __forceinline__ void q8_to_f2(uint2 q, int e, float2 (&v)[4]) {
+    const uint32_t w[4] = {q.x, q.x >> 16, q.y, q.y >> 16};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const __half2_raw r = __nv_cvt_fp8x2_to_halfraw2(__nv_fp8x2_storage_t(w[i] & 0xFFFFu), __NV_E4M3);
+        v[i] = mul2(__half22float2(__half2(r)), both(q8_scale(e)));
+    }
+}
+
 __device__ __forceinline__ void q8_to_f(uint2 q, int e, float (&v)[8]) {
-    const float s = q8_scale(e);
-    q8_two(q.x, s, v[0], v[1]);
-    q8_two(q.x >> 16, s, v[2], v[3]);
-    q8_two(q.y, s, v[4], v[5]);
-    q8_two(q.y >> 16, s, v[6], v[7]);
+    float2 f[4];
+    q8_to_f2(q, e, f);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[2 * i] = f[i].x;
+        v[2 * i + 1] = f[i].y;
+    }
 }
 
 // Stores slice `vi` of row `row` in 8 bits.  Called by every lane of the warp: the four
