@@ -159,35 +159,46 @@ __global__ void __launch_bounds__(L == 0 ? kWideThreads : kThreads, L > 0 && K =
     const bool with_dh = a.dh != nullptr;
     // a row of the ring: 16-byte chunks of dy, h (or 8-byte chunks of h8, last) and dh, each one
     // chunk after the other for all threads
-    const int row_bytes = ring_bytes<T, K, Q8>(with_dh) * threads;
-    auto chunk = [&](int slot, int array, int k, int half) {
-        return s_ring + slot * row_bytes + ((array * K + k) * CH + half) * threads * 16 + int(threadIdx.x) * 16;
-    };
-    const int dh_at = Q8 ? 1 : 2, h8_at = 1 + (with_dh ? 1 : 0);
-    auto chunk8 = [&](int slot, int k) {
-        return s_ring + slot * row_bytes + h8_at * K * CH * threads * 16 + (k * threads + int(threadIdx.x)) * 8;
-    };
-    auto copy = [&](int64_t row, int slot) {
+    const uint32_t row_bytes = ring_bytes<T, K, Q8>(with_dh) * threads;
+    const uint32_t array_bytes = K * CH * threads * 16;
+    const uint32_t dh_at = (Q8 ? 1 : 2) * array_bytes, h8_at = (with_dh ? 2 : 1) * array_bytes;
+    uint8_t *mine = s_ring + threadIdx.x * 16;
+    auto chunk = [&](uint32_t at, int k, int half) { return mine + at + (k * CH + half) * threads * 16; };
+    auto chunk8 = [&](uint32_t slot, int k) { return s_ring + slot + h8_at + (k * threads + int(threadIdx.x)) * 8; };
+    bool has[K];
 #pragma unroll
-        for (int k = 0; k < K; ++k) {
-            const int vi = lane + k * lanes;
-            if (row >= a.n || vi >= slices) continue;
-            const int64_t at = row * a.c + vi * 8;
+    for (int k = 0; k < K; ++k) has[k] = lane + k * lanes < slices;
+    // offsets of this lane's first slice: of the row at work and of the row that is copied next;
+    // of its scale byte, one row ahead
+    const uint32_t rows_n = uint32_t(a.n), stride = gridDim.x * G;
+    const int64_t step = int64_t(stride) * a.c, scale_step = int64_t(stride) * rows::q8_groups(a.c);
+    uint32_t row = blockIdx.x * G + group, copy_row = row;
+    int64_t at = int64_t(row) * a.c + lane * 8, copy_at = at;
+    int64_t scale_at = int64_t(row) * rows::q8_groups(a.c) + (lane >> 2);
+    auto copy = [&](uint32_t slot) {
+        if (copy_row < rows_n) {
 #pragma unroll
-            for (int half = 0; half < CH; ++half) {
-                ptx::cp_async16(chunk(slot, 0, k, half), a.dy + at + half * 4, 16u);
-                if constexpr (!Q8) ptx::cp_async16(chunk(slot, 1, k, half), a.h + at + half * 4, 16u);
-                if (with_dh) ptx::cp_async16(chunk(slot, dh_at, k, half), a.dh + at + half * 4, 16u);
+            for (int k = 0; k < K; ++k) {
+                if (!has[k]) continue;
+                const int64_t o = copy_at + k * lanes * 8;
+#pragma unroll
+                for (int half = 0; half < CH; ++half) {
+                    ptx::cp_async16(chunk(slot, k, half), a.dy + o + half * 4, 16u);
+                    if constexpr (!Q8) ptx::cp_async16(chunk(slot + array_bytes, k, half), a.h + o + half * 4, 16u);
+                    if (with_dh) ptx::cp_async16(chunk(slot + dh_at, k, half), a.dh + o + half * 4, 16u);
+                }
+                if constexpr (Q8) ptx::cp_async8(chunk8(slot, k), a.h8 + o);
             }
-            if constexpr (Q8) ptx::cp_async8(chunk8(slot, k), a.h8 + at);
         }
         ptx::cp_async_commit();
+        copy_row += stride;
+        copy_at += step;
     };
-    auto slice = [&](int slot, int array, int k) {
+    auto slice = [&](uint32_t at_, int k) {
         Slice8<T> r;
 #pragma unroll
         for (int half = 0; half < CH; ++half) {
-            const uint4 q = *reinterpret_cast<const uint4 *>(chunk(slot, array, k, half));
+            const uint4 q = *reinterpret_cast<const uint4 *>(chunk(at_, k, half));
             r.v[4 * half] = q.x;
             r.v[4 * half + 1] = q.y;
             r.v[4 * half + 2] = q.z;
@@ -218,29 +229,26 @@ __global__ void __launch_bounds__(L == 0 ? kWideThreads : kThreads, L > 0 && K =
         for (int k = 0; k < K; ++k) weight(k, ws[k]);
     }
     const float inv_c = 1.f / float(a.c);
-    const int64_t stride = gridDim.x * int64_t(G);
     struct Small {  // the row's rstd and scale bytes, read one row ahead
         float rstd;
         int e[K];
     };
-    auto small = [&](int64_t row) {
-        Small r;
-        r.rstd = row < a.n ? __ldg(a.rstd + row) : 0.f;
+    auto small = [&](uint32_t r) {
+        Small m;
+        m.rstd = r < rows_n ? __ldg(a.rstd + r) : 0.f;
         if constexpr (Q8) {
 #pragma unroll
-            for (int k = 0; k < K; ++k) {
-                const int vi = lane + k * lanes;
-                r.e[k] = row < a.n && vi < slices ? __ldg(a.h8s + row * rows::q8_groups(a.c) + (vi >> 2)) : 1;
-            }
+            for (int k = 0; k < K; ++k) m.e[k] = r < rows_n && has[k] ? __ldg(a.h8s + scale_at + (k * lanes >> 2)) : 1;
+            scale_at += scale_step;
         }
-        return r;
+        return m;
     };
-    int slot = 0, ahead = D - 1;
+    uint32_t slot = 0, ahead = (D - 1) * row_bytes;  // byte offsets in the ring
     // slice k of d = rstd dy, of h, and of g = rstd dy w
     auto terms = [&](const Small &m, int k, float2 (&d)[4], float2 (&h)[4], float2 (&g)[4]) {
-        rows::to_f2(slice(slot, 0, k), d);
+        rows::to_f2(slice(slot, k), d);
         if constexpr (Q8) rows::q8_to_f2(*reinterpret_cast<const uint2 *>(chunk8(slot, k)), m.e[k], h);
-        else rows::to_f2(slice(slot, 1, k), h);
+        else rows::to_f2(slice(slot + array_bytes, k), h);
         float2 w[4];
         if constexpr (!kKeepW) weight(k, w);
 #pragma unroll
@@ -250,19 +258,19 @@ __global__ void __launch_bounds__(L == 0 ? kWideThreads : kThreads, L > 0 && K =
         }
     };
     int turn = 0;
-    const int64_t first = blockIdx.x * int64_t(G);
 #pragma unroll
-    for (int d = 0; d < D - 1; ++d) copy(first + d * stride + group, d);
-    Small cur = small(first + group);
-    for (int64_t row0 = first; row0 < a.n; row0 += stride) {
-        const int64_t row = row0 + group;
-        copy(row + (D - 1) * stride, ahead);
+    for (int d = 0; d < D - 1; ++d) copy(d * row_bytes);
+    Small cur = small(row);
+    // every group of a block takes as many turns as the first one: they meet in row_sum
+    for (uint32_t row0 = blockIdx.x * G; row0 < rows_n; row0 += stride) {
+        copy(ahead);
         const Small next = small(row + stride);
         ptx::cp_async_wait<D - 1>();
+        const bool in = row < rows_n;
         float2 sum = both(0.f), h[kKeep ? K : 1][4], g[kKeep ? K : 1][4];
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            if (row >= a.n || lane + k * lanes >= slices) continue;
+            if (!in || !has[k]) continue;
             constexpr int S = kKeep ? 1 : 0;
             float2 d[4];
             terms(cur, k, d, h[S * k], g[S * k]);
@@ -273,31 +281,33 @@ __global__ void __launch_bounds__(L == 0 ? kWideThreads : kThreads, L > 0 && K =
             }
         }
         // dx = g - h rstd^2 mean(g h) + dh
-        const float at = row_sum<L>(sum.x + sum.y, s_sum, turn) * inv_c * cur.rstd * cur.rstd;
+        const float2 back = both(-row_sum<L>(sum.x + sum.y, s_sum, turn) * inv_c * cur.rstd * cur.rstd);
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            if (row >= a.n || lane + k * lanes >= slices) continue;
+            if (!in || !has[k]) continue;
             constexpr int S = kKeep ? 1 : 0;
             float2 d[4];
             if constexpr (!kKeep) terms(cur, k, d, h[0], g[0]);
             if (with_dh) {
                 float2 p[4];
-                rows::to_f2(slice(slot, dh_at, k), p);
+                rows::to_f2(slice(slot + dh_at, k), p);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) g[S * k][e] = add2(g[S * k][e], p[e]);
             }
             float out[8];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const float2 o = fma2(h[S * k][e], both(-at), g[S * k][e]);
+                const float2 o = fma2(h[S * k][e], back, g[S * k][e]);
                 out[2 * e] = o.x;
                 out[2 * e + 1] = o.y;
             }
-            rows::st(a.dx + row * a.c + (lane + k * lanes) * 8, out);
+            rows::st(a.dx + at + k * lanes * 8, out);
         }
         cur = next;
-        slot = slot + 1 == D ? 0 : slot + 1;
-        ahead = ahead + 1 == D ? 0 : ahead + 1;
+        row += stride;
+        at += step;
+        slot = slot + row_bytes == D * row_bytes ? 0 : slot + row_bytes;
+        ahead = ahead + row_bytes == D * row_bytes ? 0 : ahead + row_bytes;
     }
     ptx::cp_async_wait<0>();
     if (!a.partial) return;
