@@ -435,9 +435,10 @@ lat_status lat_q8_unpack(const void *q, const void *scale, int64_t n, int32_t c,
                          lat_stream stream);
 
 /* lat_sconv_wgrad with x (map->n_in, cin) in 8 bits: dW[k] = sum over pairs
- * (i, j) of offset k of (q * scale)[i]^T dy[j], fp32.  dtype is dy's; scale
- * 4-byte aligned.  Limits, determinism and errors as for lat_sconv_wgrad;
- * on the tensor cores 148 shares. */
+ * (i, j) of offset k of (q * scale)[i]^T dy[j], fp32.  dtype is dy's (16-byte
+ * aligned, fp32 32); scale 4-byte aligned.  Limits and errors as for
+ * lat_sconv_wgrad.  Deterministic in the same way; the number of shares
+ * depends on the pair count and the channel counts alone. */
 size_t lat_sconv_wgrad_q8_ws_bytes(int32_t cin, int32_t cout, const lat_kmap *map, lat_dtype dtype);
 lat_status lat_sconv_wgrad_q8(const void *q, const void *scale, int32_t cin, const void *dy, int32_t cout,
                               const lat_kmap *map, float *dw, lat_dtype dtype, void *ws, size_t ws_bytes,

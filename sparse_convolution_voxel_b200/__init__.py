@@ -24,6 +24,7 @@ A training step that keeps 8-bit checkpoints instead of rows:
 """
 from __future__ import annotations
 
+import contextlib
 from collections import namedtuple
 
 import torch
@@ -278,31 +279,21 @@ def to_dense(coords, feats, origin, shape, batch: int, d_status=None, out=None, 
     return grid
 
 
-class _on:
-    """Makes `stream` (a torch.cuda.Stream or a raw handle; None: leave it) the current stream, so that
-    the buffers a helper allocates belong to the stream that its kernels run on."""
+_here = contextlib.nullcontext()
 
-    def __init__(self, stream, device):
-        self.guard = None
-        if stream is not None:
-            if isinstance(stream, int):
-                stream = torch.cuda.ExternalStream(stream, device)
-            self.guard = torch.cuda.stream(stream)
 
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
+def _on(stream, device):
+    """A context in which `stream` (a torch.cuda.Stream or a raw handle; None: leave it) is the current
+    stream, so that the buffers a helper allocates belong to the stream that its kernels run on."""
+    if stream is None:
+        return _here
+    return torch.cuda.stream(torch.cuda.ExternalStream(stream, device) if isinstance(stream, int) else stream)
 
 
 def embed_fwd(ids, table, scale: float = 1.0, pad_id: int = -1, d_status=None, out=None, stream=None):
     """scale * table[ids] (n, c); rows whose id is pad_id are 0.  ids int32 or int64 (n,)."""
     with _on(stream, table.device):
-        y = out if out is not None else torch.empty((ids.shape[0], table.shape[1]), dtype=table.dtype,
-                                                    device=table.device)
+        y = out if out is not None else table.new_empty((ids.shape[0], table.shape[1]))
         lat_embed_fwd(ids, table, scale, pad_id, y, d_status, stream)
     return y
 
@@ -311,7 +302,7 @@ def embed_wgrad(ids, dy, vocab: int, scale: float = 1.0, pad_id: int = -1, ws: W
                 out=None, stream=None):
     """The table's gradient (vocab, c) in fp32: scale * the sum of dy's rows of each token."""
     with _on(stream, dy.device):
-        dt = out if out is not None else torch.empty((int(vocab), dy.shape[1]), dtype=torch.float32, device=dy.device)
+        dt = out if out is not None else dy.new_empty((vocab, dy.shape[1]), dtype=torch.float32)
         if dt.shape[0] != vocab:
             raise ValueError(f"out has {dt.shape[0]} rows, not {vocab}")
         ws = ws or Workspace(dy.device)
@@ -334,6 +325,13 @@ class Q8Rows:
         return cls(torch.empty((n, c), dtype=torch.float8_e4m3fn, device=device),
                    torch.empty((n, -(-c // LAT_Q8_GROUP)), dtype=torch.uint8, device=device))
 
+    @classmethod
+    def like(cls, x: torch.Tensor) -> "Q8Rows":
+        """Room for the rows of x."""
+        n, c = x.shape
+        return cls(x.new_empty((n, c), dtype=torch.float8_e4m3fn),
+                   x.new_empty((n, -(-c // LAT_Q8_GROUP)), dtype=torch.uint8))
+
     @property
     def shape(self):
         return self.q.shape
@@ -346,7 +344,7 @@ class Q8Rows:
 def q8_pack(x, out: Q8Rows | None = None, stream=None) -> Q8Rows:
     """x (n, c) as 8-bit rows."""
     with _on(stream, x.device):
-        r = out if out is not None else Q8Rows.empty(x.shape[0], x.shape[1], x.device)
+        r = out if out is not None else Q8Rows.like(x)
         lat_q8_pack(x, r.q, r.scale, stream)
     return r
 
@@ -354,7 +352,7 @@ def q8_pack(x, out: Q8Rows | None = None, stream=None) -> Q8Rows:
 def q8_unpack(rows: Q8Rows, dtype: torch.dtype = torch.bfloat16, out=None, stream=None):
     """The values of 8-bit rows in dtype."""
     with _on(stream, rows.q.device):
-        x = out if out is not None else torch.empty(rows.q.shape, dtype=dtype, device=rows.q.device)
+        x = out if out is not None else torch.empty_like(rows.q, dtype=dtype)
         lat_q8_unpack(rows.q, rows.scale, x, stream)
     return x
 
@@ -363,7 +361,7 @@ def conv_wgrad_q8(x: Q8Rows, dy, kmap: KernelMap, ws: Workspace | None = None, d
     """conv_wgrad with the convolution's input rows in 8 bits."""
     cin, cout = x.q.shape[1], dy.shape[1]
     with _on(stream, dy.device):
-        dw = out if out is not None else torch.empty((kmap.k3, cin, cout), dtype=torch.float32, device=dy.device)
+        dw = out if out is not None else dy.new_empty((kmap.k3, cin, cout), dtype=torch.float32)
         ws = ws or Workspace(dy.device)
         lat_sconv_wgrad_q8(x.q, x.scale, dy, kmap.c, dw,
                            ws.get(lat_sconv_wgrad_q8_ws_bytes(cin, cout, kmap.c, dy.dtype)), d_status, stream)
@@ -380,13 +378,12 @@ def rms_norm_fwd(x, w=None, res=None, eps: float = 1e-6, rows: bool = True, q8: 
     y is None without ``rows``, y8 (y in 8 bits) without ``q8`` and h8 (h in 8 bits, for rms_norm_bwd)
     without ``q8_h``.  h is x itself without ``res``; ``h_out`` (x or res, to add in place, or another
     tensor) receives h."""
-    n, c = x.shape
     with _on(stream, x.device):
         h = h_out if h_out is not None else torch.empty_like(x) if res is not None else None
         y = torch.empty_like(x) if rows else None
-        rstd = torch.empty(n, dtype=torch.float32, device=x.device)
-        y8 = Q8Rows.empty(n, c, x.device) if q8 else None
-        h8 = Q8Rows.empty(n, c, x.device) if q8_h else None
+        rstd = x.new_empty(x.shape[:1], dtype=torch.float32)
+        y8 = Q8Rows.like(x) if q8 else None
+        h8 = Q8Rows.like(x) if q8_h else None
         lat_rms_norm_fwd(x, res, w, eps, h, y, y8.q if q8 else None, y8.scale if q8 else None, h8.q if q8_h else None,
                          h8.scale if q8_h else None, rstd, stream)
     return RmsNorm(y, x if h is None else h, rstd, y8, h8)
@@ -397,7 +394,7 @@ def rms_norm_bwd(dy, h, rstd, w=None, dh=None, want_dw: bool = True, ws: Workspa
     alike, with dh (the gradient that reaches h past the norm) added; dw in fp32, None without ``want_dw``."""
     with _on(stream, dy.device):
         dx = out if out is not None else torch.empty_like(dy)
-        dw = torch.empty(dy.shape[1], dtype=torch.float32, device=dy.device) if want_dw else None
+        dw = dy.new_empty(dy.shape[1:], dtype=torch.float32) if want_dw else None
         buf = None
         if want_dw:
             ws = ws or Workspace(dy.device)

@@ -302,152 +302,158 @@ def lat_to_dense(coords, feats, origin, shape, batch: int, out, d_status=None, s
     _check(rc, "lat_to_dense")
 
 
-def _rows(x, what: str, n=None, c=None, dtype=None, like=None):
-    """Checks one argument of a row-wise entry point: 2-D, of shape (n, c), of dtype, on like's device."""
-    if x.dim() != 2 or (n is not None and x.shape[0] != n) or (c is not None and x.shape[1] != c):
-        raise ValueError(f"{what} has shape {tuple(x.shape)}, not ({'n' if n is None else n}, {'c' if c is None else c})")
-    if x.dtype != dtype if dtype is not None else x.dtype not in _DTYPE_CODE:
-        raise ValueError(f"{what} has type {x.dtype}, not {dtype or 'float32, float16 or bfloat16'}")
-    _same_device(x, what, like)
+# The row-wise entry points check their tensors here: _rows / _like give the pointer of a tensor
+# of the right shape, type and layout on the call's device, and _launch_stream, last, refuses
+# a call whose tensors are not on the current device, to whose stream the kernels go.
+def _like(t, what: str, shape, dtype, dev: int):
+    if t.shape != shape or t.dtype != dtype or t.get_device() != dev or not t.is_contiguous():
+        if tuple(t.shape) != tuple(shape):
+            raise ValueError(f"{what} has shape {tuple(t.shape)}, not {tuple(shape)}")
+        if t.dtype != dtype:
+            raise ValueError(f"{what} has type {t.dtype}, not {dtype}")
+        if t.get_device() != dev:
+            raise ValueError(f"{what} is on {t.device}, the call's other tensors on another device")
+        raise ValueError("liblattice takes contiguous tensors")
+    return t.data_ptr()
 
 
-def _vector(x, what: str, n, dtype, like):
-    if x.dim() != 1 or x.shape[0] != n or x.dtype not in (dtype if isinstance(dtype, tuple) else (dtype,)):
-        raise ValueError(f"{what} is {x.dtype} {tuple(x.shape)}, not {dtype} ({n},)")
-    _same_device(x, what, like)
+def _opt(t, what: str, shape, dtype, dev: int):
+    return None if t is None else _like(t, what, shape, dtype, dev)
 
 
-def _same_device(x, what: str, like):
-    """All tensors of a call lie on one device, which is the current one (the launch goes to the current device's stream)."""
-    if x.is_cuda:
-        here = like.device.index if like is not None else (_cur_dev() if _cur_dev is not None else
-                                                            torch.cuda.current_device())
-        if x.device.index != here:
-            raise ValueError(f"{what} is on {x.device}, the call on cuda:{here}: use torch.cuda.device")
+def _rows(x, what: str):
+    """(pointer, shape, dtype code, device) of the (n, c) rows that set a call's type and device."""
+    shape = x.shape
+    if len(shape) != 2:
+        raise ValueError(f"{what} has shape {tuple(shape)}, not (n, c)")
+    code = _DTYPE_CODE.get(x.dtype)
+    if code is None:
+        raise ValueError(f"{what} has type {x.dtype}, not float32, float16 or bfloat16")
+    if not x.is_contiguous():
+        raise ValueError("liblattice takes contiguous tensors")
+    return x.data_ptr(), shape, code, x.get_device()
 
 
-def _scratch(ws, like):
-    """(pointer, bytes) of a workspace on like's device."""
-    if ws is not None:
-        _same_device(ws, "ws", like)
-    return _ws_args(ws)
+def _ids(ids, n: int, dev: int):
+    size = 4 if ids.dtype == torch.int32 else 8 if ids.dtype == torch.int64 else 0
+    if not size:
+        raise ValueError(f"ids has type {ids.dtype}, not int32 or int64")
+    return _like(ids, "ids", (n,), ids.dtype, dev), size
 
 
-def _status_word(d_status, like):
-    if d_status is not None:
-        _vector(d_status, "d_status", 1, torch.int32, like)
+def _q8(q, scale, what: str, n: int, c: int, dev: int):
+    """Pointers of 8-bit rows; (None, None) for none."""
+    if q is None and scale is None:
+        return None, None
+    if q is None or scale is None:
+        raise ValueError(f"{what} needs its values and its scales")
+    return (_like(q, what, (n, c), torch.float8_e4m3fn, dev),
+            _like(scale, what + " scale", (n, -(-c // LAT_Q8_GROUP)), torch.uint8, dev))
 
 
-def _q8_rows(q, scale, what: str, like, n=None, c=None):
-    _rows(q, what, n, c, torch.float8_e4m3fn, like)
-    _rows(scale, what + " scale", q.shape[0], -(-q.shape[1] // LAT_Q8_GROUP), torch.uint8, like if like is not None else q)
+def _scratch(ws, dev: int):
+    if ws is None:
+        return None, 0
+    if ws.get_device() != dev or not ws.is_contiguous():
+        raise ValueError("ws is a contiguous buffer on the call's device")
+    return ws.data_ptr(), ws.numel() * ws.element_size()
+
+
+def _launch_stream(dev: int, stream):
+    if dev < 0:
+        raise ValueError("liblattice takes device tensors")
+    here = _cur_dev() if _cur_dev is not None else torch.cuda.current_device()
+    if dev != here:
+        raise ValueError(f"the tensors are on cuda:{dev}, the current device is cuda:{here}: use torch.cuda.device")
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(here)
+    return _stream(stream)
 
 
 def lat_embed_fwd(ids, table, scale: float, pad_id: int, y, d_status=None, stream=None):
-    _rows(table, "table")
-    _vector(ids, "ids", ids.shape[0] if ids.dim() == 1 else -1, (torch.int32, torch.int64), table)
-    _rows(y, "y", ids.shape[0], table.shape[1], table.dtype, table)
-    _status_word(d_status, table)
-    rc = load().lat_embed_fwd(_ptr(ids), ids.element_size(), ids.shape[0], _ptr(table), table.shape[0], table.shape[1],
-                              float(scale), int(pad_id), _ptr(y), dtype_code(table.dtype), _ptr(d_status),
-                              _stream(stream))
+    tp, (vocab, c), code, dev = _rows(table, "table")
+    n = y.shape[0]
+    ip, size = _ids(ids, n, dev)
+    rc = load().lat_embed_fwd(ip, size, n, tp, vocab, c, scale, pad_id, _like(y, "y", (n, c), table.dtype, dev), code,
+                              _opt(d_status, "d_status", (1,), torch.int32, dev), _launch_stream(dev, stream))
     _check(rc, "lat_embed_fwd")
 
 
 def lat_embed_wgrad_ws_bytes(n: int, vocab: int, c: int) -> int:
-    return int(load().lat_embed_wgrad_ws_bytes(int(n), int(vocab), int(c)))
+    return int(load().lat_embed_wgrad_ws_bytes(n, vocab, c))
 
 
 def lat_embed_wgrad(ids, dy, scale: float, pad_id: int, dtable, ws=None, d_status=None, stream=None):
-    _rows(dy, "dy")
-    _vector(ids, "ids", dy.shape[0], (torch.int32, torch.int64), dy)
-    _rows(dtable, "dtable", None, dy.shape[1], torch.float32, dy)
-    _status_word(d_status, dy)
-    p, n = _scratch(ws, dy)
-    rc = load().lat_embed_wgrad(_ptr(ids), ids.element_size(), ids.shape[0], _ptr(dy), dtable.shape[0], dy.shape[1],
-                                float(scale), int(pad_id), _ptr(dtable), dtype_code(dy.dtype), p, n, _ptr(d_status),
-                                _stream(stream))
+    dp, (n, c), code, dev = _rows(dy, "dy")
+    ip, size = _ids(ids, n, dev)
+    vocab = dtable.shape[0]
+    wp, wn = _scratch(ws, dev)
+    rc = load().lat_embed_wgrad(ip, size, n, dp, vocab, c, scale, pad_id,
+                                _like(dtable, "dtable", (vocab, c), torch.float32, dev), code, wp, wn,
+                                _opt(d_status, "d_status", (1,), torch.int32, dev), _launch_stream(dev, stream))
     _check(rc, "lat_embed_wgrad")
 
 
 def lat_q8_pack(x, q, scale, stream=None):
-    _rows(x, "x")
-    _q8_rows(q, scale, "q", x, *x.shape)
-    rc = load().lat_q8_pack(_ptr(x), x.shape[0], x.shape[1], _ptr(q), _ptr(scale), dtype_code(x.dtype),
-                            _stream(stream))
+    xp, (n, c), code, dev = _rows(x, "x")
+    qp, sp = _q8(q, scale, "q", n, c, dev)
+    rc = load().lat_q8_pack(xp, n, c, qp, sp, code, _launch_stream(dev, stream))
     _check(rc, "lat_q8_pack")
 
 
 def lat_q8_unpack(q, scale, x, stream=None):
-    _rows(x, "x")
-    _q8_rows(q, scale, "q", x, *x.shape)
-    rc = load().lat_q8_unpack(_ptr(q), _ptr(scale), x.shape[0], x.shape[1], _ptr(x), dtype_code(x.dtype),
-                              _stream(stream))
+    xp, (n, c), code, dev = _rows(x, "x")
+    qp, sp = _q8(q, scale, "q", n, c, dev)
+    rc = load().lat_q8_unpack(qp, sp, n, c, xp, code, _launch_stream(dev, stream))
     _check(rc, "lat_q8_unpack")
 
 
 def lat_sconv_wgrad_q8_ws_bytes(cin: int, cout: int, kmap: lat_kmap, dtype: torch.dtype) -> int:
-    return int(load().lat_sconv_wgrad_q8_ws_bytes(int(cin), int(cout), ctypes.byref(kmap), dtype_code(dtype)))
+    return int(load().lat_sconv_wgrad_q8_ws_bytes(cin, cout, ctypes.byref(kmap), dtype_code(dtype)))
 
 
 def lat_sconv_wgrad_q8(q, scale, dy, kmap: lat_kmap, dw, ws=None, d_status=None, stream=None):
-    _rows(dy, "dy", kmap.n_out)
-    _q8_rows(q, scale, "q", dy, kmap.n_in)
-    cin, cout = q.shape[1], dy.shape[1]
-    if dw.dtype != torch.float32 or tuple(dw.shape) != (kmap.k3, cin, cout):
-        raise ValueError(f"dw is {dw.dtype} {tuple(dw.shape)}, not float32 {(kmap.k3, cin, cout)}")
-    _same_device(dw, "dw", dy)
-    _status_word(d_status, dy)
-    p, n = _scratch(ws, dy)
-    rc = load().lat_sconv_wgrad_q8(_ptr(q), _ptr(scale), cin, _ptr(dy), cout, ctypes.byref(kmap), _ptr(dw),
-                                   dtype_code(dy.dtype), p, n, _ptr(d_status), _stream(stream))
+    gp, (n_out, cout), code, dev = _rows(dy, "dy")
+    if n_out != kmap.n_out:
+        raise ValueError(f"dy has shape {(n_out, cout)}, not {(kmap.n_out, cout)}")
+    cin = q.shape[1]
+    qp, sp = _q8(q, scale, "q", kmap.n_in, cin, dev)
+    wp, wn = _scratch(ws, dev)
+    rc = load().lat_sconv_wgrad_q8(qp, sp, cin, gp, cout, ctypes.byref(kmap),
+                                   _like(dw, "dw", (kmap.k3, cin, cout), torch.float32, dev), code, wp, wn,
+                                   _opt(d_status, "d_status", (1,), torch.int32, dev), _launch_stream(dev, stream))
     _check(rc, "lat_sconv_wgrad_q8")
 
 
 def lat_rms_norm_fwd(x, res, w, eps: float, h=None, y=None, y8=None, y8_scale=None, h8=None, h8_scale=None, rstd=None,
                      stream=None):
-    _rows(x, "x")
-    n, c = x.shape
-    for t, what in ((res, "res"), (h, "h"), (y, "y")):
-        if t is not None:
-            _rows(t, what, n, c, x.dtype, x)
-    for q, s, what in ((y8, y8_scale, "y8"), (h8, h8_scale, "h8")):
-        if (q is None) != (s is None):
-            raise ValueError(f"{what} needs its values and its scales")
-        if q is not None:
-            _q8_rows(q, s, what, x, n, c)
-    if w is not None:
-        _vector(w, "w", c, x.dtype, x)
-    if rstd is not None:
-        _vector(rstd, "rstd", n, torch.float32, x)
-    rc = load().lat_rms_norm_fwd(_ptr(x), _ptr(res), _ptr(w), n, c, float(eps), _ptr(h), _ptr(y), _ptr(y8),
-                                 _ptr(y8_scale), _ptr(h8), _ptr(h8_scale), _ptr(rstd), dtype_code(x.dtype),
-                                 _stream(stream))
+    xp, shape, code, dev = _rows(x, "x")
+    n, c = shape
+    dt = x.dtype
+    y8p, y8s = _q8(y8, y8_scale, "y8", n, c, dev)
+    h8p, h8s = _q8(h8, h8_scale, "h8", n, c, dev)
+    rc = load().lat_rms_norm_fwd(xp, _opt(res, "res", shape, dt, dev), _opt(w, "w", (c,), dt, dev), n, c, eps,
+                                 _opt(h, "h", shape, dt, dev), _opt(y, "y", shape, dt, dev), y8p, y8s, h8p, h8s,
+                                 _opt(rstd, "rstd", (n,), torch.float32, dev), code, _launch_stream(dev, stream))
     _check(rc, "lat_rms_norm_fwd")
 
 
 def lat_rms_norm_bwd_ws_bytes(n: int, c: int) -> int:
-    return int(load().lat_rms_norm_bwd_ws_bytes(int(n), int(c)))
+    return int(load().lat_rms_norm_bwd_ws_bytes(n, c))
 
 
 def lat_rms_norm_bwd(dy, dh, h, h8, h8_scale, rstd, w, dx, dw=None, ws=None, stream=None):
-    _rows(dy, "dy")
-    n, c = dy.shape
-    if (h is None) == (h8 is None) or (h8 is None) != (h8_scale is None):
+    dp, shape, code, dev = _rows(dy, "dy")
+    n, c = shape
+    dt = dy.dtype
+    if (h is None) == (h8 is None):
         raise ValueError("rms_norm_bwd takes h, or its 8-bit values and their scales")
-    for t, what in ((dh, "dh"), (h, "h"), (dx, "dx")):
-        if t is not None:
-            _rows(t, what, n, c, dy.dtype, dy)
-    if h8 is not None:
-        _q8_rows(h8, h8_scale, "h8", dy, n, c)
-    _vector(rstd, "rstd", n, torch.float32, dy)
-    if w is not None:
-        _vector(w, "w", c, dy.dtype, dy)
-    if dw is not None:
-        _vector(dw, "dw", c, torch.float32, dy)
-    p, nb = _scratch(ws, dy)
-    rc = load().lat_rms_norm_bwd(_ptr(dy), _ptr(dh), _ptr(h), _ptr(h8), _ptr(h8_scale), _ptr(rstd), _ptr(w), n, c,
-                                 _ptr(dx), _ptr(dw), dtype_code(dy.dtype), p, nb, _stream(stream))
+    h8p, h8s = _q8(h8, h8_scale, "h8", n, c, dev)
+    wp, wn = _scratch(ws, dev)
+    rc = load().lat_rms_norm_bwd(dp, _opt(dh, "dh", shape, dt, dev), _opt(h, "h", shape, dt, dev), h8p, h8s,
+                                 _like(rstd, "rstd", (n,), torch.float32, dev), _opt(w, "w", (c,), dt, dev), n, c,
+                                 _like(dx, "dx", shape, dt, dev), _opt(dw, "dw", (c,), torch.float32, dev), code, wp,
+                                 wn, _launch_stream(dev, stream))
     _check(rc, "lat_rms_norm_bwd")
 
 

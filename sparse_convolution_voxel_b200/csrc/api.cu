@@ -101,16 +101,10 @@ extern "C" lat_status lat_sconv_wgrad(const void *x, int32_t cin, const void *dy
     });
 }
 
-// Shapes that the tensor cores take read the 8-bit rows themselves; for the others the
-// rows are unpacked into dy's type, in front of lat_sconv_wgrad's own workspace.
-static size_t q8_rows_bytes(int32_t cin, const lat_kmap *map, lat_dtype dtype) {
-    return lat::align_up(size_t(map->n_in) * size_t(cin) * (dtype == LAT_F32 ? 4 : 2), 256);
-}
-
 extern "C" size_t lat_sconv_wgrad_q8_ws_bytes(int32_t cin, int32_t cout, const lat_kmap *map, lat_dtype dtype) {
     if (!lat::map_ok(map) || !lat::chan_ok(cin, dtype) || !lat::chan_ok(cout, dtype)) return 0;
-    if (dtype != LAT_F32 && lat::wgrad_tc_supported(cin, cout)) return lat::wgrad_q8_tc_ws_bytes(cin, cout, map);
-    return q8_rows_bytes(cin, map, dtype) + lat_sconv_ws_bytes(LAT_OP_WGRAD, cin, cout, map, dtype);
+    return (dtype != LAT_F32 && lat::wgrad_tc_supported(cin, cout)) ? lat::wgrad_q8_tc_ws_bytes(cin, cout, map)
+                                                                    : lat::wgrad_q8_simt_ws_bytes(cin, cout, map);
 }
 
 extern "C" lat_status lat_sconv_wgrad_q8(const void *q, const void *scale, int32_t cin, const void *dy, int32_t cout,
@@ -120,19 +114,20 @@ extern "C" lat_status lat_sconv_wgrad_q8(const void *q, const void *scale, int32
     if (!map_ok(map) || !chan_ok(cin, dtype) || !chan_ok(cout, dtype) || !dw || !map->pair_off) return LAT_ERR_ARG;
     if (dtype != LAT_F32 && dtype != LAT_F16 && dtype != LAT_BF16) return LAT_ERR_ARG;
     if (map->n_in > 0 && (!q || !scale)) return LAT_ERR_ARG;
-    if (!aligned16(q) || reinterpret_cast<uintptr_t>(scale) % 4 || !aligned16(dy) || !aligned16(dw)) return LAT_ERR_ARG;
+    const uintptr_t slice = dtype == LAT_F32 ? 32 : 16;
+    if (!aligned16(q) || reinterpret_cast<uintptr_t>(scale) % 4 || reinterpret_cast<uintptr_t>(dy) % slice ||
+        !aligned16(dw))
+        return LAT_ERR_ARG;
     if (map->pair_capacity > 0 && (!map->pair_in || !map->pair_out)) return LAT_ERR_ARG;
     if (!ws || !aligned16(ws) || ws_bytes < lat_sconv_wgrad_q8_ws_bytes(cin, cout, map, dtype))
         return LAT_ERR_WORKSPACE;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     if (dtype != LAT_F32 && wgrad_tc_supported(cin, cout))
-        return launch_wgrad_q8_tc(dtype == LAT_BF16, q, scale, cin, dy, cout, map, dw, ws, d_status,
-                                  reinterpret_cast<cudaStream_t>(stream));
-    const lat_status st =
-        launch_q8_unpack(q, scale, map->n_in, cin, ws, dtype, reinterpret_cast<cudaStream_t>(stream));
-    if (st != LAT_OK) return st;
-    const size_t used = q8_rows_bytes(cin, map, dtype);
-    return lat_sconv_wgrad(ws, cin, dy, cout, map, dw, dtype, static_cast<char *>(ws) + used, ws_bytes - used, d_status,
-                           stream);
+        return launch_wgrad_q8_tc(dtype == LAT_BF16, q, scale, cin, dy, cout, map, dw, ws, d_status, s);
+    return by_dtype(dtype, [&](auto t) {
+        using T = decltype(t);
+        return launch_wgrad_q8_simt<T>(q, scale, cin, dy, cout, map, dw, ws, d_status, s);
+    });
 }
 
 extern "C" int32_t lat_status_fetch(const int32_t *d_status, lat_stream stream) {

@@ -68,8 +68,12 @@ bool wgrad_tc_supported(int cin, int cout);
 size_t wgrad_tc_ws_bytes(int cin, int cout, const lat_kmap *map);
 lat_status launch_wgrad_tc(bool bf16, const void *x, int cin, const void *dy, int cout, const lat_kmap *map, float *dw,
                            void *ws, int32_t *d_status, cudaStream_t s);
-lat_status launch_q8_unpack(const void *q, const void *scale, int64_t n, int c, void *x, lat_dtype dtype,
-                            cudaStream_t s);
+lat_status launch_wgrad_q8_reduce(const float *partial, const int32_t *ranges, int nelem, int k3, float *dw,
+                                  cudaStream_t s);
+size_t wgrad_q8_simt_ws_bytes(int cin, int cout, const lat_kmap *map);
+template <typename T>
+lat_status launch_wgrad_q8_simt(const void *q, const void *scale, int cin, const void *dy, int cout,
+                                const lat_kmap *map, float *dw, void *ws, int32_t *d_status, cudaStream_t s);
 size_t wgrad_q8_tc_ws_bytes(int cin, int cout, const lat_kmap *map);
 lat_status launch_wgrad_q8_tc(bool bf16, const void *q, const void *scale, int cin, const void *dy, int cout,
                               const lat_kmap *map, float *dw, void *ws, int32_t *d_status, cudaStream_t s);

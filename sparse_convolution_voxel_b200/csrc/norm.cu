@@ -363,8 +363,10 @@ __global__ void __launch_bounds__(1024) norm_dw_kernel(const float *__restrict__
 
 // Calls f with the row layout for c channels: lanes per row (0: a block), slices per
 // lane, and the threads of a block.
+// few: fewer rows than SMs, where a row's latency counts (4 x 4096: 3.5 us with one slice per
+// lane, 5.0 with two).
 template <typename F>
-static lat_status by_layout(int c, F &&f) {
+static lat_status by_layout(int c, bool few, F &&f) {
     const int slices = c / 8;
     auto threads = [&](int k) { return (slices + 32 * k - 1) / (32 * k) * 32; };
     using std::integral_constant;
@@ -373,7 +375,8 @@ static lat_status by_layout(int c, F &&f) {
     if (slices <= 16) return f(integral_constant<int, 16>{}, integral_constant<int, 1>{}, kThreads);
     if (slices <= 32) return f(integral_constant<int, 32>{}, integral_constant<int, 1>{}, kThreads);
     if (slices <= 64) return f(integral_constant<int, 32>{}, integral_constant<int, 2>{}, kThreads);
-    if (slices <= 128) return f(integral_constant<int, 0>{}, integral_constant<int, 1>{}, threads(1));
+    if (slices <= 128 || (few && slices <= kWideThreads))
+        return f(integral_constant<int, 0>{}, integral_constant<int, 1>{}, threads(1));
     if (slices <= 1024) return f(integral_constant<int, 0>{}, integral_constant<int, 2>{}, threads(2));
     return f(integral_constant<int, 0>{}, integral_constant<int, 4>{}, threads(4));
 }
@@ -399,7 +402,7 @@ lat_status fwd(const void *x, const void *res, const void *w, int64_t n, int c, 
              static_cast<T *>(y), static_cast<uint8_t *>(y8), static_cast<uint8_t *>(y8s), static_cast<uint8_t *>(h8),
              static_cast<uint8_t *>(h8s), rstd, n, c, eps};
     const int64_t per = rows_per_block(c);
-    return by_layout(c, [&](auto l, auto k, int threads) -> lat_status {
+    return by_layout(c, n < num_sms(), [&](auto l, auto k, int threads) -> lat_status {
         LAT_CUDA_TRY(launch_pdl(norm_fwd_kernel<T, decltype(l)::value, decltype(k)::value>,
                                 dim3(unsigned((n + per - 1) / per)), dim3(threads), 0, s, a));
         return LAT_OK;
@@ -413,7 +416,7 @@ lat_status bwd(const void *dy, const void *dh, const void *h, const void *h8, co
              static_cast<const T *>(dh), static_cast<const uint8_t *>(h8), static_cast<const uint8_t *>(h8s), rstd,
              static_cast<T *>(dx), dw ? partial : nullptr, n, c};
     const int64_t blocks = shares(n, c);
-    const lat_status st = by_layout(c, [&](auto l, auto k, int threads) -> lat_status {
+    const lat_status st = by_layout(c, false, [&](auto l, auto k, int threads) -> lat_status {
         constexpr int L = decltype(l)::value, K = decltype(k)::value;
         auto go = [&](auto kern, size_t row_bytes) -> lat_status {
             const size_t sums = L == 0 ? 0 : sizeof(float) * size_t(kThreads / (L == 0 ? 1 : L)) * size_t(c);

@@ -128,19 +128,6 @@ lat_status unpack(const uint8_t *q, const uint8_t *scale, int64_t n, int c, void
 }
 
 }  // namespace q8
-
-lat_status launch_q8_unpack(const void *q, const void *scale, int64_t n, int c, void *x, lat_dtype dtype,
-                            cudaStream_t s) {
-    const uint8_t *qb = static_cast<const uint8_t *>(q), *sb = static_cast<const uint8_t *>(scale);
-    if (n == 0) return LAT_OK;
-    switch (dtype) {
-        case LAT_F32: return q8::unpack<float>(qb, sb, n, c, x, s);
-        case LAT_F16: return q8::unpack<__half>(qb, sb, n, c, x, s);
-        case LAT_BF16: return q8::unpack<__nv_bfloat16>(qb, sb, n, c, x, s);
-    }
-    return LAT_ERR_ARG;
-}
-
 }  // namespace lat
 
 extern "C" lat_status lat_q8_pack(const void *x, int64_t n, int32_t c, void *q, void *scale, lat_dtype dtype,
@@ -168,5 +155,13 @@ extern "C" lat_status lat_q8_unpack(const void *q, const void *scale, int64_t n,
     if (dtype != LAT_F32 && dtype != LAT_F16 && dtype != LAT_BF16) return LAT_ERR_ARG;
     if (n > 0 && (!x || !q || !scale)) return LAT_ERR_ARG;
     if (!rows::aligned(x, rows::slice_bytes(dtype)) || !rows::aligned(q, 16)) return LAT_ERR_ARG;
-    return launch_q8_unpack(q, scale, n, c, x, dtype, reinterpret_cast<cudaStream_t>(stream));
+    if (n == 0) return LAT_OK;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    const uint8_t *qb = static_cast<const uint8_t *>(q), *sb = static_cast<const uint8_t *>(scale);
+    switch (dtype) {
+        case LAT_F32: return q8::unpack<float>(qb, sb, n, c, x, s);
+        case LAT_F16: return q8::unpack<__half>(qb, sb, n, c, x, s);
+        case LAT_BF16: return q8::unpack<__nv_bfloat16>(qb, sb, n, c, x, s);
+    }
+    return LAT_ERR_ARG;
 }

@@ -363,6 +363,7 @@ wgrad_q8_reduce_kernel(const float *__restrict__ partial, const int32_t *__restr
     const int k = blockIdx.y;
     const int v0 = __ldg(ranges + 2 * k), v1 = __ldg(ranges + 2 * k + 1);
     const int el = (blockIdx.x * 32 + threadIdx.x) * 4;
+    const bool in = el < nelem;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     auto add = [&](const float4 &x) {
         acc.x += x.x;
@@ -371,11 +372,11 @@ wgrad_q8_reduce_kernel(const float *__restrict__ partial, const int32_t *__restr
         acc.w += x.w;
     };
 #pragma unroll 8
-    for (int v = v0 + int(threadIdx.y); v <= v1; v += kRedRows)
+    for (int v = v0 + int(threadIdx.y); in && v <= v1; v += kRedRows)
         add(__ldg(reinterpret_cast<const float4 *>(partial + int64_t(v + k) * nelem + el)));
     s[threadIdx.y][threadIdx.x] = acc;
     __syncthreads();
-    if (threadIdx.y == 0) {
+    if (threadIdx.y == 0 && in) {
 #pragma unroll
         for (int r = 1; r < kRedRows; ++r) add(s[r][threadIdx.x]);
         *reinterpret_cast<float4 *>(dw + int64_t(k) * nelem + el) = acc;
@@ -396,13 +397,19 @@ static lat_status launch(const uint8_t *q, const uint8_t *scale, const void *dy,
     LAT_CUDA_TRY(launch_pdl(kern, dim3(unsigned(grid)), dim3(kThreads), C::kSmem, s, q, scale,
                             static_cast<const T *>(dy), map->pair_off, map->pair_in, map->pair_out, map->pair_capacity,
                             map->k3, map->n_in, map->n_out, partial, ranges, wait_limit_ns(), d_status));
-    constexpr int nelem = M * N;
-    LAT_CUDA_TRY(launch_pdl(wgrad_q8_reduce_kernel, dim3(nelem / 128, unsigned(map->k3)), dim3(32, kRedRows), 0, s,
-                            partial, ranges, nelem, dw));
-    return LAT_OK;
+    return launch_wgrad_q8_reduce(partial, ranges, M * N, map->k3, dw, s);
 }
 
 }  // namespace wq8
+
+// dw[k] from the partials of nelem floats (a multiple of 4) at slots share + k; ranges[k]: the
+// first and the last share that meets offset k.
+lat_status launch_wgrad_q8_reduce(const float *partial, const int32_t *ranges, int nelem, int k3, float *dw,
+                                  cudaStream_t s) {
+    LAT_CUDA_TRY(launch_pdl(wq8::wgrad_q8_reduce_kernel, dim3(unsigned((nelem + 127) / 128), unsigned(k3)),
+                            dim3(32, wq8::kRedRows), 0, s, partial, ranges, nelem, dw));
+    return LAT_OK;
+}
 
 size_t wgrad_q8_tc_ws_bytes(int cin, int cout, const lat_kmap *map) {
     Carver cv(nullptr);
