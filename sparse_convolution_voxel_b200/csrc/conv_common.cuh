@@ -1,6 +1,8 @@
 // Kernel-map view shared by the convolution kernels.
 #pragma once
 
+#include <cuda.h>
+
 #include <algorithm>
 
 #include "common.cuh"
@@ -74,6 +76,7 @@ size_t wgrad_q8_simt_ws_bytes(int cin, int cout, const lat_kmap *map);
 template <typename T>
 lat_status launch_wgrad_q8_simt(const void *q, const void *scale, int cin, const void *dy, int cout,
                                 const lat_kmap *map, float *dw, void *ws, int32_t *d_status, cudaStream_t s);
+bool tensor_map_2d(CUtensorMap *map, const void *p, bool bf16, int64_t rows, int cols, int box_cols, int box_rows);
 size_t wgrad_q8_tc_ws_bytes(int cin, int cout, const lat_kmap *map);
 lat_status launch_wgrad_q8_tc(bool bf16, const void *q, const void *scale, int cin, const void *dy, int cout,
                               const lat_kmap *map, float *dw, void *ws, int32_t *d_status, cudaStream_t s);

@@ -547,18 +547,27 @@ static EncodeFn encode_fn() {
     return fn;
 }
 
-// Weights (k3, wrows, wcols) row-major viewed as a 2D (k3*wrows) x wcols tensor, 64 x 64 boxes, 128-byte swizzle.
-static bool make_weight_map(CUtensorMap *map, const void *w, bool bf16, int k3, int wrows, int wcols) {
-    EncodeFn enc = encode_fn();
+}  // namespace tc
+
+// A row-major 2D tensor of 16-bit elements, boxes of box_cols (64: the 128-byte swizzle) x box_rows.
+bool tensor_map_2d(CUtensorMap *map, const void *p, bool bf16, int64_t rows, int cols, int box_cols, int box_rows) {
+    tc::EncodeFn enc = tc::encode_fn();
     if (!enc) return false;
-    const cuuint64_t dims[2] = {cuuint64_t(wcols), cuuint64_t(k3) * wrows};
-    const cuuint64_t strides[1] = {cuuint64_t(wcols) * 2};
-    const cuuint32_t box[2] = {64, 64};
+    const cuuint64_t dims[2] = {cuuint64_t(cols), cuuint64_t(rows)};
+    const cuuint64_t strides[1] = {cuuint64_t(cols) * 2};
+    const cuuint32_t box[2] = {cuuint32_t(box_cols), cuuint32_t(box_rows)};
     const cuuint32_t estr[2] = {1, 1};
     return enc(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,
-               const_cast<void *>(w), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               const_cast<void *>(p), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+namespace tc {
+
+// Weights (k3, wrows, wcols) row-major viewed as a 2D (k3*wrows) x wcols tensor, 64 x 64 boxes, 128-byte swizzle.
+static bool make_weight_map(CUtensorMap *map, const void *w, bool bf16, int k3, int wrows, int wcols) {
+    return tensor_map_2d(map, w, bf16, int64_t(k3) * wrows, wcols, 64, 64);
 }
 
 // The weight tensor map of (w, shape, type), remembered per host thread for the

@@ -9,19 +9,20 @@
 // 4 significant bits and a power of two: bf16 holds it exactly.  fp16 rounds values below
 // 2^-14 to its subnormals' steps and is held at 65504.
 //
-// One CTA per SM.  Two groups of eight warps take the blocks of 64 pairs in turn, each with
-// an A tile, a ring of kDy dy tiles and a ring of kRaw raw x blocks of its own.  A group
-// copies raw x chunks, scale bytes and dy rows (dy straight into its swizzled tile) with
-// cp.async three of its blocks ahead; each thread widens the chunks that it copied itself
-// -- only its own cp.async groups to wait for, no barrier -- into the A tile and arrives at
-// the tile's barrier, on which the MMA warp waits.  The commit of a block's MMAs frees the
-// A tile and the dy tile.  (One group of eight warps with two A tiles took 95 us at 500k
-// rows, 128 -> 128: a chain of latencies in two warps per scheduler.)
+// One CTA per SM, every role of its own:
+//   * two groups of eight warps widen the blocks of 64 pairs in turn, each with two A tiles
+//     and a ring of kRing blocks (raw x rows, scale bytes, dy tile) of its own: wait for the
+//     block's copies, widen x into an A tile, arrive at the tile's barrier.  (One group took
+//     95 us at 500k rows, 128 -> 128: a chain of latencies in two warps per scheduler.)
+//   * four warps gather the blocks' rows with cp.async, dy straight into its swizzled tile.
+//   * one thread fetches the blocks that are a run: three quarters of a scan's pairs are
+//     (j, j), the centre of a submanifold map, in row order, so that 64 pairs are 64
+//     consecutive rows: bulk copies of x and the scales, a tensor copy per 64 channels of dy.
+//   * one thread issues the MMAs, whose commits free the A tile and the ring slot, and four
+//     warps store each segment's sum from TMEM.
+// With the gathers in the widening warps, which then wait for one another's latencies, it
+// took 76 us, as now NN us.
 //
-// A segment's sum leaves TMEM every kFlush blocks: the tensor cores cut bits off when they
-// add, and over a share of thousands of pairs in one accumulator that would be the largest
-// error of the result.  Four warps add it in fp32 to the segment's partial, which the same
-// thread wrote.
 #include <algorithm>
 
 #include "conv_common.cuh"
@@ -33,16 +34,22 @@ namespace lat {
 namespace wq8 {
 
 constexpr int kKP = 64;        // pairs per block (GEMM K block)
-constexpr int kWorkers = 148;  // shares of the pair list: one per B200 SM
+// The pair list is cut into equal contiguous shares of at least a block, at most kTurns for
+// each of kWorkers workers (one per B200 SM); worker w takes the shares w, w + kWorkers, ....
+// So the gathers, which a scan's map has at both ends of its list, are spread over all
+// workers: in one share each, the CTAs with gathers alone took 77 us and the others 53.
+constexpr int kWorkers = 148, kTurns = 4;
 constexpr int kGroups = 2, kGroupWarps = 8;
-constexpr int kProdWarps = kGroups * kGroupWarps, kEpiWarps = 4;
-constexpr int kGroupThreads = kGroupWarps * 32;
-constexpr int kAhead = 3;                   // blocks that a group copies ahead
-constexpr int kDy = kAhead + 1, kRaw = kAhead;  // slots of its rings
-constexpr int kMmaWarp = kProdWarps + kEpiWarps;
-constexpr int kThreads = (kMmaWarp + 1) * 32;
-constexpr int kPairs = kKP / kGroupWarps;  // pairs of a block that one warp copies
-constexpr int kFlush = 32;                // blocks per TMEM sum
+constexpr int kWideWarps = kGroups * kGroupWarps, kEpiWarps = 4, kGatherWarps = 4;
+constexpr int kGroupThreads = kGroupWarps * 32, kGatherThreads = kGatherWarps * 32;
+constexpr int kRing = 3;      // blocks in a group's ring
+constexpr int kTiles = 2;     // A tiles of a group
+constexpr int kLook = 4;      // blocks whose pairs are read ahead
+constexpr int kScaleBytes = kKP * 4 + 32;  // of a ring slot: a word per pair, or a run's bytes from a 16-byte boundary
+constexpr int kGatherAt = kWideWarps + kEpiWarps;  // first gathering warp
+constexpr int kMmaWarp = kGatherAt + kGatherWarps, kLoadWarp = kMmaWarp + 1;
+constexpr int kThreads = (kLoadWarp + 1) * 32;
+constexpr int kWidePairs = kKP / kGroupWarps, kGatherPairs = kKP / kGatherWarps;  // of a block, per warp
 constexpr uint64_t kDrainNs = 1000000000ull;  // limit of the waits that drain a CTA that gave up
 
 template <int M, int N>
@@ -50,26 +57,105 @@ struct Cfg {
     static constexpr uint32_t kABytes = uint32_t(M) * 128;  // 64 pairs x M channels x 2 bytes
     static constexpr uint32_t kBBytes = uint32_t(N) * 128;
     static constexpr uint32_t kXBytes = uint32_t(M) * 64;   // raw
-    static constexpr uint32_t kDyAt = kGroups * kABytes;        // the A tiles, then the dy tiles, raw x, scales
-    static constexpr uint32_t kRawAt = kDyAt + kGroups * kDy * kBBytes;
-    static constexpr uint32_t kScaleAt = kRawAt + kGroups * kRaw * kXBytes;  // 4 bytes per pair
-    static constexpr uint32_t kBars = kScaleAt + kGroups * kRaw * kKP * 4;
+    static constexpr uint32_t kDyAt = kGroups * kTiles * kABytes;        // the A tiles, then the dy tiles, raw x, scales
+    static constexpr uint32_t kRawAt = kDyAt + kGroups * kRing * kBBytes;
+    static constexpr uint32_t kScaleAt = kRawAt + kGroups * kRing * kXBytes;
+    static constexpr uint32_t kBars = kScaleAt + kGroups * kRing * kScaleBytes;
     static constexpr uint32_t kSmem = kBars + 256 + 1024;
     static constexpr uint32_t kTmemCols = 2 * N;
     static constexpr int kChunks = M / 64;  // 16-byte raw chunks per thread and block
 };
 template <typename T, int M, int N> struct KernelTag {};  // one launch-config cache per kernel
 
-// Walks the blocks of this CTA's segments.
+// A worker's pairs of one offset in one of its shares, in the order in which it takes them.
+// Segments of one offset that follow one another are one sum: one accumulator, one partial.
+struct Segment {
+    int64_t lo, hi;  // pairs
+    int k, slot;     // offset, partial
+    bool begins, ends;  // the sum
+};
+constexpr int kMaxSegments = kTurns + 32;  // every segment ends a share or an offset
+
+// The worker's segments, made by one warp: lane k looks at offset k.
+struct Work {
+    int64_t off[33];  // offset k has pairs [off[k], off[k + 1])
+    int64_t cut[kTurns][2];
+    int count;
+    Segment seg[kMaxSegments];
+    __device__ void make(const int64_t *pair_off, int64_t capacity, int k3, int worker, int32_t *ranges) {
+        const int lane = threadIdx.x & 31;
+        for (int e = lane; e <= k3; e += 32) off[e] = min(pair_off[e], capacity);
+        __syncwarp();
+        const int64_t P = off[k3];
+        const int S = int(max(int64_t(P > 0), min(int64_t(kWorkers * kTurns), P / kKP)));
+        if (lane < 2 * kTurns) {  // share v has pairs [P v / S, P (v + 1) / S)
+            const int v = worker + lane / 2 * kWorkers;
+            cut[lane / 2][lane & 1] = v < S ? P * (v + (lane & 1)) / S : 0;
+        }
+        // the shares and the workers that meet this lane's offset: pair p is in share floor((S (p + 1) - 1) / P)
+        const int64_t a = lane < k3 ? off[lane] : 0, b = lane < k3 ? off[lane + 1] : 0;
+        int parts = 0, first = 0;
+        if (a < b) {
+            const int v0 = int((S * (a + 1) - 1) / P), v1 = int((S * b - 1) / P);
+            parts = min(v1 - v0 + 1, kWorkers);
+            first = parts < kWorkers ? v0 % kWorkers : 0;
+        }
+        int upto = parts;
+#pragma unroll
+        for (int m = 1; m < 32; m <<= 1) {
+            const int u = __shfl_up_sync(0xFFFFFFFFu, upto, m);
+            if (lane >= m) upto += u;
+        }
+        if (ranges && lane < k3) {
+            ranges[2 * lane] = upto - parts;
+            ranges[2 * lane + 1] = upto - 1;
+        }
+        const int slot = upto - parts + (worker - first + kWorkers) % kWorkers;
+        __syncwarp();
+        int n = 0;
+        for (int t = 0; t < kTurns; ++t) {
+            const int64_t lo = max(a, cut[t][0]), hi = min(b, cut[t][1]);
+            const uint32_t some = __ballot_sync(0xFFFFFFFFu, lo < hi);
+            if (lo < hi) seg[n + __popc(some & ((1u << lane) - 1u))] = Segment{lo, hi, lane, slot, true, true};
+            n += __popc(some);
+        }
+        __syncwarp();
+        for (int i = lane; i < n; i += 32) {
+            seg[i].begins = i == 0 || seg[i - 1].k != seg[i].k;
+            seg[i].ends = i == n - 1 || seg[i + 1].k != seg[i].k;
+        }
+        if (lane == 0) count = n;
+    }
+};
+
+// Walks the blocks of the segments.  A block is a run if its pairs are 64 consecutive rows
+// whose scale bytes (G per row) can be copied from a 16-byte boundary: the full blocks of the
+// centre, but for the last rows' bytes.
+template <int G>
 struct Blocks {
-    wtc::Segments<kWorkers> seg;
-    int64_t p0 = 0, hi = 0;
-    __device__ Blocks(const int64_t *off, int k3) : seg(off, k3) {}
-    __device__ bool next() {  // pairs [p0, min(p0 + kKP, hi))
+    const Work &work;
+    int64_t p0 = 0, hi = 0, run_end = 0, row0 = 0;  // pairs [p0, min(p0 + kKP, hi)); row0: p0's row in the centre
+    int64_t rows;
+    int s = 0, centre;
+    bool run = false;
+    __device__ Blocks(const Work &w, int centre_, int64_t rows_) : work(w), rows(rows_), centre(centre_) {}
+    __device__ __forceinline__ bool next() {
         p0 += kKP;
-        if (p0 < hi) return true;
-        int k, slot;
-        return seg.next(k, p0, hi, slot);
+        row0 += kKP;
+        if (p0 >= hi) {
+            if (s == work.count) return false;
+            const Segment &g = work.seg[s++];
+            p0 = g.lo;
+            hi = g.hi;
+            run_end = -1;
+            if (g.k == centre) {
+                row0 = p0 - work.off[g.k];
+                // full blocks, inside the rows, and floor16(row G) + 64 G + 16 <= rows G
+                run_end = min(hi - kKP, work.off[g.k] + min(rows - kKP, rows - kKP - (16 + G - 1) / G));
+            }
+        }
+        run = p0 <= run_end;
+        return true;
     }
 };
 
@@ -85,7 +171,7 @@ __device__ __forceinline__ uint4 widen(uint2 q, int e) {
 
 template <typename T, int M, int N>
 __global__ void __launch_bounds__(kThreads, 1)
-wgrad_q8_kernel(const uint8_t *__restrict__ q, const uint8_t *__restrict__ scale, const T *__restrict__ dy,
+wgrad_q8_kernel(const __grid_constant__ CUtensorMap dy_map, int centre, const uint8_t *__restrict__ q, const uint8_t *__restrict__ scale, const T *__restrict__ dy,
                 const int64_t *__restrict__ pair_off, const int32_t *__restrict__ pair_in,
                 const int32_t *__restrict__ pair_out, int64_t capacity, int k3, int64_t n_in, int64_t n_out,
                 float *__restrict__ partial, int32_t *__restrict__ ranges, uint64_t wait_ns, int32_t *d_status) {
@@ -96,34 +182,34 @@ wgrad_q8_kernel(const uint8_t *__restrict__ q, const uint8_t *__restrict__ scale
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::kBars);
-    uint64_t *empty = full + kGroups;
-    uint64_t *accfull = empty + kGroups;
+    uint64_t *empty = full + kGroups * kTiles;    // A tiles
+    uint64_t *freed = empty + kGroups * kTiles;   // ring slots
+    uint64_t *accfull = freed + kGroups * kRing;
     uint64_t *accempty = accfull + 2;
-    uint64_t *drain = accempty + 2;  // tracks the MMAs still in flight when a CTA gives up
+    uint64_t *landed = accempty + 2;  // bulk and tensor copies, [group][slot]
+    uint64_t *drain = landed + kGroups * kRing;  // tracks the MMAs still in flight when a CTA gives up
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
     __shared__ int s_abort;
-    __shared__ int64_t s_off[33];
-    __shared__ uint8_t s_odd[kGroups * kRaw][kKP];  // M = 64: the pair's scale bytes are the upper half of their word
+    __shared__ Work s_work;
+    __shared__ uint8_t s_odd[kGroups * kRing][kKP];  // M = 64: the pair's scale bytes are the upper half of their word
+    __shared__ int s_last[kGroups * kRing];          // parity of the slot's phase if its last block is a run, else -1
+    __shared__ int s_run[kGroups * kRing];           // the block is a run: where its scale bytes begin, else -1
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    if (warp == 1) {
-        wtc::load_offsets(pair_off, capacity, k3, s_off);
-        __syncwarp();
-        if (blockIdx.x == 0 && lane < k3) {
-            // for the reduce: the shares meeting offset lane's pairs [a, b)
-            const int64_t P = s_off[k3], a = s_off[lane], b = s_off[lane + 1];
-            ranges[2 * lane] = a < b ? wtc::share_of<kWorkers>(P, a) : 0;
-            ranges[2 * lane + 1] = a < b ? wtc::share_of<kWorkers>(P, b - 1) : -1;
-        }
-    }
+    if (warp == 1) s_work.make(pair_off, capacity, k3, int(blockIdx.x), blockIdx.x == 0 ? ranges : nullptr);
     if (tid == 0) {
-        for (int s = 0; s < kGroups; ++s) {
+        for (int s = 0; s < kGroups * kTiles; ++s) {
             ptx::mbar_init(&full[s], kGroupThreads);
             ptx::mbar_init(&empty[s], 1);
         }
         for (int s = 0; s < 2; ++s) {
             ptx::mbar_init(&accfull[s], 1);
             ptx::mbar_init(&accempty[s], kEpiWarps * 32);
+        }
+        for (int s = 0; s < kGroups * kRing; ++s) {
+            ptx::mbar_init(&landed[s], 1 + kGatherThreads);
+            ptx::mbar_init(&freed[s], 1);
+            s_last[s] = -1;
         }
         ptx::mbar_init(drain, 1);
         s_abort = 0;
@@ -140,107 +226,54 @@ wgrad_q8_kernel(const uint8_t *__restrict__ q, const uint8_t *__restrict__ scale
     const uint32_t tmem_base = *tmem_slot;
     int32_t bad = 0;
 
-    if (warp < kProdWarps) {
-        // ------------------------------------------------------------ copy ahead, widen x
-        constexpr int XL = M / 16;       // lanes per raw x row
-        constexpr int XP = 32 / XL;      // rows per warp and chunk
-        const int grp = warp / kGroupWarps, gw = warp % kGroupWarps, gt = tid % kGroupThreads;
-        const int xc = lane % XL, xg = lane / XL;
-        const int g = lane >> 3, c = lane & 7;
-        Blocks blk(s_off, k3);
-        bool have = blk.next();
-        for (int i = 0; i < grp; ++i) have = have && blk.next();
-        int si = -1, sj = -1;
-        auto fetch = [&]() {  // lanes 0..7: the indices of this warp's pairs of the group's next block
-            const int64_t mp = blk.p0 + gw * kPairs + lane;
-            si = sj = -1;
-            if (have && lane < kPairs && mp < blk.hi) {
-                si = __ldg(pair_in + mp);
-                sj = __ldg(pair_out + mp);
-            }
-        };
-        fetch();
-        uint32_t issued = 0;
-        auto issue = [&]() {  // copies of the group's next block, one cp.async group (empty past the last block)
-            if (have) {
-                if (si >= n_in || sj >= n_out || (si < 0) != (sj < 0)) {
-                    bad |= LAT_ERR_BAD_MAP;
-                    si = sj = -1;
-                }
-                const uint32_t r = grp * kRaw + issued % kRaw;
-                uint8_t *xs = smem + C::kRawAt + r * C::kXBytes;
-                uint8_t *Bs = smem + C::kDyAt + (grp * kDy + issued % kDy) * C::kBBytes;
-                if (lane < kPairs) {
-                    const int p = gw * kPairs + lane;
-                    const int64_t at = si < 0 ? 0 : int64_t(si) * (M / 32), word = at & ~int64_t(3);
-                    const int64_t left = n_in * (M / 32) - word;
-                    ptx::cp_async4(smem + C::kScaleAt + (r * kKP + p) * 4, scale + word,
-                                   si < 0 ? 0u : uint32_t(left < 4 ? left : 4));
-                    if (M == 64) s_odd[r][p] = uint8_t(at & 2);
-                }
-#pragma unroll
-                for (int i = 0; i < C::kChunks; ++i) {
-                    const int ii = __shfl_sync(0xFFFFFFFFu, si, i * XP + xg);
-                    const uint8_t *src = ii >= 0 ? q + int64_t(ii) * M + xc * 16 : q;
-                    ptx::cp_async16(xs + (i * kGroupThreads + gt) * 16, src, ii >= 0 ? 16u : 0u);
-                }
-#pragma unroll
-                for (int i = 0; i < kPairs / 4; ++i) {
-                    const int pl = 4 * i + g, p = gw * kPairs + pl;
-                    const int jj = __shfl_sync(0xFFFFFFFFu, sj, pl);
-                    const uint32_t off = (p >> 3) * 1024 + (p & 7) * 128 + ((c ^ (p & 7)) << 4);
-#pragma unroll
-                    for (int nb = 0; nb < N / 64; ++nb) {
-                        const T *src = jj >= 0 ? dy + int64_t(jj) * N + nb * 64 + c * 8 : dy;
-                        ptx::cp_async16(Bs + nb * 8192 + off, src, jj >= 0 ? 16u : 0u);
-                    }
-                }
-                ++issued;
-                for (int i = 0; i < kGroups; ++i) have = have && blk.next();
-                fetch();
-            }
-            ptx::cp_async_commit();
-        };
-#pragma unroll 1
-        for (int d = 0; d < kAhead; ++d) issue();
-        uint8_t *As = smem + grp * C::kABytes;
+    if (warp < kWideWarps) {
+        // ------------------------------------------------------------ widen x
+        constexpr int XL = M / 16, XP = 32 / XL;  // lanes per raw x row, rows per warp and chunk
+        const int grp = warp / kGroupWarps, gw = warp % kGroupWarps, xc = lane % XL, xg = lane / XL;
+        // 16-byte chunks 2 xc and 2 xc + 1 of a pair's row; the upper half of the lanes stores them the other way
+        // round, so that eight lanes meet eight different banks
+        const int mb = xc >> 2, cc = (2 * xc) & 7;
+        const bool turn = mb & 1;
+        const int first = cc + (turn ? 1 : 0), second = cc + (turn ? 0 : 1);
+        uint32_t blocks = 0;  // of this group
+        for (int i = 0; i < s_work.count; ++i)
+            blocks += uint32_t((s_work.seg[i].hi - s_work.seg[i].lo + kKP - 1) / kKP);
+        blocks = (blocks + kGroups - 1 - grp) / kGroups;
+        uint32_t slot = 0, phase = 0;  // the block's ring slot, and the slot's phase
         bool ok = true;
 #pragma unroll 1
-        for (uint32_t it = 0; it < issued; ++it) {
-            // the MMAs of the group's previous block: they read the A tile and the dy tile that issue() refills
-            if (!__all_sync(0xFFFFFFFFu, ptx::mbar_wait(&empty[grp], (it & 1) ^ 1, wait_ns))) {
+        for (uint32_t it = 0; it < blocks; ++it) {
+            const uint32_t r = grp * kRing + slot, t = grp * kTiles + it % kTiles;
+            // this block's copies, and the MMAs that read the A tile last
+            if (!__all_sync(0xFFFFFFFFu, ptx::mbar_wait(&landed[r], phase, wait_ns) &&
+                                             ptx::mbar_wait(&empty[t], ((it / kTiles) & 1) ^ 1, wait_ns))) {
                 ok = false;
                 break;
             }
-            ptx::cp_async_wait<kAhead - 1>();
-            __syncwarp();
-            const uint32_t r = grp * kRaw + it % kRaw;
-            const uint8_t *xs = smem + C::kRawAt + r * C::kXBytes;
-            const uint32_t *ss = reinterpret_cast<const uint32_t *>(smem + C::kScaleAt) + r * kKP;
+            const uint8_t *xs = smem + C::kRawAt + r * C::kXBytes + (gw * kWidePairs + xg) * M + xc * 16;
+            const uint8_t *ss = smem + C::kScaleAt + r * kScaleBytes;
+            const int from = s_run[r];
+            uint8_t *row = smem + t * C::kABytes + mb * 8192 + gw * 1024;  // kWidePairs == 8: one 8-pair atom per warp
 #pragma unroll
             for (int i = 0; i < C::kChunks; ++i) {
-                const int p = gw * kPairs + i * XP + xg;
-                const uint4 raw = *reinterpret_cast<const uint4 *>(xs + (i * kGroupThreads + gt) * 16);
-                const int shift = 8 * (xc >> 1) + (M == 64 ? 8 * s_odd[r][p] : 0);  // channels 16 xc ..
-                const int e = (ss[p] >> shift) & 0xFF;
+                const int sw = i * XP + xg, p = gw * kWidePairs + sw;
+                const uint4 raw = *reinterpret_cast<const uint4 *>(xs + i * XP * M);
+                // channels 16 xc .. 16 xc + 15
+                const int e = ss[(from >= 0 ? from + p * (M / 32) : p * 4 + (M == 64 ? s_odd[r][p] : 0)) + (xc >> 1)];
                 const uint4 lo = widen<T>(make_uint2(raw.x, raw.y), e), hi = widen<T>(make_uint2(raw.z, raw.w), e);
-                // 16-byte chunks 2 xc and 2 xc + 1 of the pair's row; the upper half of the lanes stores them the
-                // other way round, so that eight lanes meet eight different banks
-                const int mb = xc >> 2, cc = (2 * xc) & 7, sw = p & 7;
-                uint8_t *row = As + mb * 8192 + (p >> 3) * 1024 + sw * 128;
-                const bool turn = mb & 1;
-                *reinterpret_cast<uint4 *>(row + (((cc + (turn ? 1 : 0)) ^ sw) << 4)) = turn ? hi : lo;
-                *reinterpret_cast<uint4 *>(row + (((cc + (turn ? 0 : 1)) ^ sw) << 4)) = turn ? lo : hi;
+                *reinterpret_cast<uint4 *>(row + sw * 128 + ((first ^ sw) << 4)) = turn ? hi : lo;
+                *reinterpret_cast<uint4 *>(row + sw * 128 + ((second ^ sw) << 4)) = turn ? lo : hi;
             }
-            // the tile and this thread's dy chunks, written through the generic proxy, before the tensor cores' reads
+            // the tile, written through the generic proxy, before the tensor cores' reads
             ptx::fence_proxy_async_smem();
-            ptx::mbar_arrive(&full[grp]);
-            __syncwarp();  // the raw block and the scales are read: issue() refills them
-            issue();
+            ptx::mbar_arrive(&full[t]);
+            if (++slot == kRing) {
+                slot = 0;
+                phase ^= 1;
+            }
         }
-        ptx::cp_async_wait<0>();
         if (!ok) s_abort = 1;
-    } else if (warp < kMmaWarp) {
+    } else if (warp < kGatherAt) {
         // ------------------------------------------------------------ epilogue: partial of each segment
         const int quad = warp & 3;
         // M = 128: lane l of quadrant w holds row 32w + l; M = 64: lanes 0..15 hold rows 16w + l
@@ -248,84 +281,204 @@ wgrad_q8_kernel(const uint8_t *__restrict__ q, const uint8_t *__restrict__ scale
         const bool has_row = M == 128 || lane < 16;
         uint32_t ta = 0;
         bool ok = true;
-        wtc::Segments<kWorkers> seg(s_off, k3);
-        int k, slot;
-        int64_t lo, hi;
-        while (ok && seg.next(k, lo, hi, slot)) {
-            float *dst = partial + int64_t(slot) * M * N + int64_t(row) * N;
-            for (int64_t p = lo; p < hi; p += kFlush * kKP) {
-                const uint32_t a = ta & 1;
-                if (!__all_sync(0xFFFFFFFFu, ptx::mbar_wait(&accfull[a], (ta >> 1) & 1, wait_ns))) {
-                    ok = false;
-                    break;
-                }
-                ptx::tc_fence_after();
-                const uint32_t taddr = tmem_base + (uint32_t(quad * 32) << 16) + a * N;
+        for (int i = 0; i < s_work.count; ++i) {
+            if (!s_work.seg[i].ends) continue;
+            float *dst = partial + int64_t(s_work.seg[i].slot) * M * N + int64_t(row) * N;
+            const uint32_t a = ta & 1;
+            if (!__all_sync(0xFFFFFFFFu, ptx::mbar_wait(&accfull[a], (ta >> 1) & 1, wait_ns))) {
+                ok = false;
+                break;
+            }
+            ptx::tc_fence_after();
+            const uint32_t taddr = tmem_base + (uint32_t(quad * 32) << 16) + a * N;
 #pragma unroll
-                for (int c0 = 0; c0 < N; c0 += 16) {
-                    uint32_t v[16];
-                    ptx::tmem_ld16(taddr + c0, v);
-                    ptx::tmem_wait_ld();
-                    if (has_row) {
-                        float4 *d4 = reinterpret_cast<float4 *>(dst + c0);
+            for (int c0 = 0; c0 < N; c0 += 32) {
+                uint32_t v[2][16];
+                ptx::tmem_ld16(taddr + c0, v[0]);
+                ptx::tmem_ld16(taddr + c0 + 16, v[1]);
+                ptx::tmem_wait_ld();
+                if (has_row) {
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            float4 o = make_float4(__uint_as_float(v[4 * e]), __uint_as_float(v[4 * e + 1]),
-                                                   __uint_as_float(v[4 * e + 2]), __uint_as_float(v[4 * e + 3]));
-                            if (p != lo) {
-                                const float4 was = d4[e];
-                                o = make_float4(o.x + was.x, o.y + was.y, o.z + was.z, o.w + was.w);
-                            }
-                            d4[e] = o;
-                        }
+                    for (int e = 0; e < 4; ++e) {
+                        const uint32_t *w = v[e / 2] + 8 * (e % 2);
+                        const uint32_t o[8] = {w[0], w[1], w[2], w[3], w[4], w[5], w[6], w[7]};
+                        ptx::st_global_v8(dst + c0 + 8 * e, o);
                     }
                 }
-                ptx::tc_fence_before();
-                ptx::mbar_arrive(&accempty[a]);
-                ++ta;
             }
+            ptx::tc_fence_before();
+            ptx::mbar_arrive(&accempty[a]);
+            ++ta;
         }
         if (!ok) s_abort = 1;
-    } else if (lane == 0) {
+    } else if (warp < kMmaWarp) {
+        // ------------------------------------------------------------ gather rows
+        constexpr int XL = M / 16, XP = 32 / XL;
+        const int gw = warp - kGatherAt, xc = lane % XL, xg = lane / XL, g = lane >> 3, c = lane & 7;
+        Blocks<M / 32> blk(s_work, centre, n_in);
+        // lanes 0..15: the indices of this warp's pairs of the next kLook blocks (a run needs none), so that their
+        // own latency, as long as a block's work, is not met once per block
+        int si[kLook], sj[kLook];
+        bool have[kLook], run[kLook];
+        auto fetch = [&](int u) {
+            si[u] = sj[u] = -1;
+            have[u] = blk.next();
+            run[u] = blk.run;
+            if (!have[u] || run[u]) return;
+            const int64_t mp = blk.p0 + gw * kGatherPairs + lane;
+            if (lane < kGatherPairs && mp < blk.hi) {
+                si[u] = __ldg(pair_in + mp);
+                sj[u] = __ldg(pair_out + mp);
+            }
+        };
+#pragma unroll
+        for (int u = 0; u < kLook; ++u) {
+            have[u] = false;
+            if (u == 0 || have[u - 1]) fetch(u);
+        }
+        bool ok = true;
+        uint32_t grp = 0, slot = 0, phase = 1;  // the wait for the slot's previous block; the first ones pass
+        auto gather = [&](int u) -> bool {
+            const uint32_t r = grp * kRing + slot;
+            if (!__all_sync(0xFFFFFFFFu, ptx::mbar_wait(&freed[r], phase, wait_ns))) return false;
+            if (!run[u]) {
+                int ri = si[u], rj = sj[u];
+                if (ri >= n_in || rj >= n_out || (ri < 0) != (rj < 0)) {
+                    bad |= LAT_ERR_BAD_MAP;
+                    ri = rj = -1;
+                }
+                uint8_t *xs = smem + C::kRawAt + r * C::kXBytes, *Bs = smem + C::kDyAt + r * C::kBBytes;
+                if (lane < kGatherPairs) {
+                    const int p = gw * kGatherPairs + lane;
+                    const int64_t at = ri < 0 ? 0 : int64_t(ri) * (M / 32), word = at & ~int64_t(3);
+                    const int64_t left = n_in * (M / 32) - word;
+                    ptx::cp_async4(smem + C::kScaleAt + r * kScaleBytes + p * 4, scale + word,
+                                   ri < 0 ? 0u : uint32_t(left < 4 ? left : 4));
+                    if (M == 64) s_odd[r][p] = uint8_t(at & 2);
+                }
+#pragma unroll
+                for (int i = 0; i < kGatherPairs / XP; ++i) {
+                    const int pl = i * XP + xg, ii = __shfl_sync(0xFFFFFFFFu, ri, pl);
+                    const uint8_t *src = ii >= 0 ? q + int64_t(ii) * M + xc * 16 : q;
+                    ptx::cp_async16(xs + (gw * kGatherPairs + pl) * M + xc * 16, src, ii >= 0 ? 16u : 0u);
+                }
+#pragma unroll
+                for (int i = 0; i < kGatherPairs / 4; ++i) {
+                    const int pl = 4 * i + g, p = gw * kGatherPairs + pl;
+                    const int jj = __shfl_sync(0xFFFFFFFFu, rj, pl);
+                    const uint32_t off = (p >> 3) * 1024 + (p & 7) * 128 + ((c ^ (p & 7)) << 4);
+                    const T *src = jj >= 0 ? dy + int64_t(jj) * N + c * 8 : dy;
+#pragma unroll
+                    for (int nb = 0; nb < N / 64; ++nb)
+                        ptx::cp_async16(Bs + nb * 8192 + off, src + (jj >= 0 ? nb * 64 : 0), jj >= 0 ? 16u : 0u);
+                }
+            }
+            ptx::cp_async_arrive_noinc(&landed[r]);  // when this thread's copies are there
+            if (++grp == kGroups) {
+                grp = 0;
+                if (++slot == kRing) {
+                    slot = 0;
+                    phase ^= 1;
+                }
+            }
+            return true;
+        };
+#pragma unroll 1
+        while (ok && have[0]) {
+#pragma unroll
+            for (int u = 0; u < kLook; ++u) {
+                if (!have[u]) break;
+                ok = gather(u);
+                if (!ok) break;
+                fetch(u);
+            }
+        }
+        ptx::cp_async_wait<0>();
+        if (!ok) s_abort = 1;
+    } else if (warp == kMmaWarp && lane == 0) {
         // ------------------------------------------------------------ MMA issue
         uint32_t it = 0, ta = 0;
         bool ok = true;
-        wtc::Segments<kWorkers> seg(s_off, k3);
-        int k, slot;
-        int64_t lo, hi;
-        while (ok && seg.next(k, lo, hi, slot)) {
-            for (int64_t p = lo; ok && p < hi; p += kFlush * kKP) {
-                const uint32_t a = ta & 1;
+        uint32_t acc = 0;
+        for (int i = 0; ok && i < s_work.count; ++i) {
+            const Segment g = s_work.seg[i];
+            const uint32_t a = ta & 1;
+            if (g.begins) {
                 if (!ptx::mbar_wait(&accempty[a], ((ta >> 1) & 1) ^ 1, wait_ns)) {
                     ok = false;
                     break;
                 }
                 ptx::tc_fence_after();
-                const uint32_t dcol = tmem_base + a * N;
-                const int64_t end = min(hi, p + kFlush * kKP);
-                uint32_t acc = 0;
-                for (int64_t p0 = p; p0 < end; p0 += kKP) {
-                    const uint32_t grp = it % kGroups, n = it / kGroups;  // block n of its group
-                    if (!ptx::mbar_wait(&full[grp], n & 1, wait_ns)) {
-                        ok = false;
-                        break;
-                    }
-                    ptx::tc_fence_after();
-                    const uint32_t as = ptx::smem_u32(smem + grp * C::kABytes);
-                    const uint32_t bs = ptx::smem_u32(smem + C::kDyAt + (grp * kDy + n % kDy) * C::kBBytes);
-#pragma unroll
-                    for (int ks = 0; ks < 4; ++ks) {
-                        const uint64_t ad = ptx::desc_sw128(as + ks * 2048, 8192, 1024);
-                        const uint64_t bd = ptx::desc_sw128(bs + ks * 2048, 8192, 1024);
-                        ptx::umma_f16(dcol, ad, bd, idesc, acc);
-                        acc = 1;
-                    }
-                    ptx::umma_commit(&empty[grp]);
-                    ++it;
+                acc = 0;
+            }
+            const uint32_t dcol = tmem_base + a * N;
+            for (int64_t p0 = g.lo; p0 < g.hi; p0 += kKP) {
+                const uint32_t grp = it % kGroups, n = it / kGroups;  // block n of its group
+                const uint32_t t = grp * kTiles + n % kTiles, r = grp * kRing + n % kRing;
+                // the widened tile; its threads have seen the dy tile land
+                if (!ptx::mbar_wait(&full[t], (n / kTiles) & 1, wait_ns)) {
+                    ok = false;
+                    break;
                 }
-                if (!ok) break;
+                ptx::tc_fence_after();
+                // the gathered dy rows were written by cp.async (generic proxy)
+                ptx::fence_proxy_async_smem();
+                const uint32_t as = ptx::smem_u32(smem + t * C::kABytes);
+                const uint32_t bs = ptx::smem_u32(smem + C::kDyAt + r * C::kBBytes);
+#pragma unroll
+                for (int ks = 0; ks < 4; ++ks) {
+                    const uint64_t ad = ptx::desc_sw128(as + ks * 2048, 8192, 1024);
+                    const uint64_t bd = ptx::desc_sw128(bs + ks * 2048, 8192, 1024);
+                    ptx::umma_f16(dcol, ad, bd, idesc, acc);
+                    acc = 1;
+                }
+                ptx::umma_commit(&empty[t]);
+                ptx::umma_commit(&freed[r]);
+                ++it;
+            }
+            if (!ok) break;
+            if (g.ends) {
                 ptx::umma_commit(&accfull[a]);
                 ++ta;
+            }
+        }
+        if (!ok) s_abort = 1;
+    } else if (warp == kLoadWarp && lane == 0) {
+        // ------------------------------------------------------------ runs of rows
+        Blocks<M / 32> blk(s_work, centre, n_in);
+        bool ok = true;
+        uint32_t grp = 0, slot = 0, phase = 1;
+        while (blk.next()) {
+            const uint32_t r = grp * kRing + slot;
+            // every block's slot is waited for, also a gathered one's: a wait knows a phase only by its
+            // parity, so the one before it must have been seen
+            if (!ptx::mbar_wait(&freed[r], phase, wait_ns)) {
+                ok = false;
+                break;
+            }
+            if (blk.run) {
+                const int64_t row0 = blk.row0, at = row0 * (M / 32);
+                constexpr uint32_t kBytes = kKP * (M / 32) + 16;
+                s_run[r] = int(at & 15);
+                s_last[r] = int(phase ^ 1);
+                ptx::mbar_arrive_expect_tx(&landed[r], C::kXBytes + C::kBBytes + kBytes);
+                ptx::bulk_load(smem + C::kRawAt + r * C::kXBytes, q + row0 * M, C::kXBytes, &landed[r]);
+                ptx::bulk_load(smem + C::kScaleAt + r * kScaleBytes, scale + (at & ~int64_t(15)), kBytes, &landed[r]);
+#pragma unroll
+                for (int nb = 0; nb < N / 64; ++nb)
+                    ptx::tma_load_2d(smem + C::kDyAt + r * C::kBBytes + nb * 8192, &dy_map, &landed[r], nb * 64,
+                                     int(row0));
+            } else {
+                s_run[r] = -1;
+                s_last[r] = -1;
+                ptx::mbar_arrive(&landed[r]);
+            }
+            if (++grp == kGroups) {
+                grp = 0;
+                if (++slot == kRing) {
+                    slot = 0;
+                    phase ^= 1;
+                }
             }
         }
         if (!ok) s_abort = 1;
@@ -333,10 +486,14 @@ wgrad_q8_kernel(const uint8_t *__restrict__ q, const uint8_t *__restrict__ scale
 
     __syncthreads();
     if (s_abort) {
-        // A role gave up: the copies are complete (cp.async.wait_all above); the MMA thread
-        // commits every MMA it issued to `drain` and waits for it (with its own limit) before
-        // the TMEM and shared memory are released.
+        // A role gave up.  Before the CTA releases its TMEM and shared memory, everything still
+        // writing into them must land: the gathers have (cp.async.wait_all above); the load
+        // thread waits for the run that a slot was given last, and the MMA thread commits every MMA it
+        // issued to `drain` and waits for it.  These waits have their own limit.
         bad |= (tid == 0) ? LAT_ERR_TIMEOUT : 0;
+        if (warp == kLoadWarp && lane == 0)
+            for (int r = 0; r < kGroups * kRing; ++r)  // (a phase whose gather warps gave up stays open: one limit for all)
+                if (s_last[r] >= 0 && !ptx::mbar_wait(&landed[r], s_last[r], kDrainNs)) break;
         if (warp == kMmaWarp && lane == 0) {
             ptx::umma_commit(drain);
             ptx::mbar_wait(drain, 0, kDrainNs);
@@ -350,36 +507,43 @@ wgrad_q8_kernel(const uint8_t *__restrict__ q, const uint8_t *__restrict__ scale
     }
 }
 
-// dW[k] = sum of offset k's partials (slots share + k, shares v0..v1 from the main kernel).
-// A block takes 32 float4 columns of dW[k]; row r of kRedRows adds the shares v0 + r,
-// v0 + r + kRedRows, ... in order, then the rows' sums are added in order.  Offsets
+// dW[k] = sum of offset k's partials, slots ranges[2 k] .. ranges[2 k + 1].  A block takes 64
+// float4 columns of dW[k], two per thread; row r of kRedRows adds the slots first + r,
+// first + r + kRedRows, ... in order, then the rows' sums are added in order.  Offsets
 // without pairs get 0.
 constexpr int kRedRows = 8;
 __global__ void __launch_bounds__(32 * kRedRows)
 wgrad_q8_reduce_kernel(const float *__restrict__ partial, const int32_t *__restrict__ ranges, int nelem,
                        float *__restrict__ dw) {
     pdl_enter();
-    __shared__ float4 s[kRedRows][32];
+    __shared__ float4 s[kRedRows][2][32];
     const int k = blockIdx.y;
     const int v0 = __ldg(ranges + 2 * k), v1 = __ldg(ranges + 2 * k + 1);
-    const int el = (blockIdx.x * 32 + threadIdx.x) * 4;
-    const bool in = el < nelem;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    auto add = [&](const float4 &x) {
-        acc.x += x.x;
-        acc.y += x.y;
-        acc.z += x.z;
-        acc.w += x.w;
+    const int el = (blockIdx.x * 64 + threadIdx.x) * 4;
+    const bool in[2] = {el < nelem, el + 128 < nelem};
+    float4 acc[2] = {};
+    auto add = [](float4 &a, const float4 &x) {
+        a.x += x.x;
+        a.y += x.y;
+        a.z += x.z;
+        a.w += x.w;
     };
-#pragma unroll 8
-    for (int v = v0 + int(threadIdx.y); in && v <= v1; v += kRedRows)
-        add(__ldg(reinterpret_cast<const float4 *>(partial + int64_t(v + k) * nelem + el)));
-    s[threadIdx.y][threadIdx.x] = acc;
-    __syncthreads();
-    if (threadIdx.y == 0 && in) {
+#pragma unroll 4
+    for (int v = v0 + int(threadIdx.y); v <= v1; v += kRedRows) {
+        const float *src = partial + int64_t(v) * nelem + el;
 #pragma unroll
-        for (int r = 1; r < kRedRows; ++r) add(s[r][threadIdx.x]);
-        *reinterpret_cast<float4 *>(dw + int64_t(k) * nelem + el) = acc;
+        for (int h = 0; h < 2; ++h)
+            if (in[h]) add(acc[h], __ldg(reinterpret_cast<const float4 *>(src + 128 * h)));
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) s[threadIdx.y][h][threadIdx.x] = acc[h];
+    __syncthreads();
+    if (threadIdx.y < 2) {
+        const int h = threadIdx.y;
+        float4 t = s[0][h][threadIdx.x];
+#pragma unroll
+        for (int r = 1; r < kRedRows; ++r) add(t, s[r][h][threadIdx.x]);
+        if (in[h]) *reinterpret_cast<float4 *>(dw + int64_t(k) * nelem + el + 128 * h) = t;
     }
 }
 
@@ -387,14 +551,20 @@ template <typename T, int M, int N>
 static lat_status launch(const uint8_t *q, const uint8_t *scale, const void *dy, const lat_kmap *map, float *dw,
                          void *ws, int32_t *d_status, cudaStream_t s) {
     using C = Cfg<M, N>;
+    constexpr bool is_bf16 = wtc::is_bf16<T>();
     Carver cv(ws);
-    float *partial = cv.take<float>(size_t(kWorkers + map->k3) * M * N);
+    float *partial = cv.take<float>(size_t(kWorkers * kTurns + map->k3) * M * N);
     int32_t *ranges = cv.take<int32_t>(64);
     auto kern = wgrad_q8_kernel<T, M, N>;
-    const int64_t grid =
-        std::min<int64_t>(kWorkers, GridCache<KernelTag<T, M, N>>::get(kern, C::kSmem, int(C::kTmemCols), 1));
-    if (grid <= 0) return LAT_ERR_CUDA;
-    LAT_CUDA_TRY(launch_pdl(kern, dim3(unsigned(grid)), dim3(kThreads), C::kSmem, s, q, scale,
+    if (GridCache<KernelTag<T, M, N>>::get(kern, C::kSmem, int(C::kTmemCols), 1) <= 0) return LAT_ERR_CUDA;
+    // in a submanifold map pair m of the centre offset is (m, m)
+    CUtensorMap dy_map = {};
+    int centre = map->mode == LAT_SUBM && map->n_in == map->n_out && map->n_out >= kKP &&
+                         reinterpret_cast<uintptr_t>(scale) % 16 == 0
+                     ? map->k3 / 2
+                     : -1;
+    if (centre >= 0 && !tensor_map_2d(&dy_map, dy, is_bf16, map->n_out, N, 64, kKP)) return LAT_ERR_CUDA;
+    LAT_CUDA_TRY(launch_pdl(kern, dim3(kWorkers), dim3(kThreads), C::kSmem, s, dy_map, centre, q, scale,
                             static_cast<const T *>(dy), map->pair_off, map->pair_in, map->pair_out, map->pair_capacity,
                             map->k3, map->n_in, map->n_out, partial, ranges, wait_limit_ns(), d_status));
     return launch_wgrad_q8_reduce(partial, ranges, M * N, map->k3, dw, s);
@@ -402,18 +572,18 @@ static lat_status launch(const uint8_t *q, const uint8_t *scale, const void *dy,
 
 }  // namespace wq8
 
-// dw[k] from the partials of nelem floats (a multiple of 4) at slots share + k; ranges[k]: the
-// first and the last share that meets offset k.
+// dw[k] from the partials of nelem floats (a multiple of 4); ranges[2 k], ranges[2 k + 1]: its first
+// and last one (first > last: none).
 lat_status launch_wgrad_q8_reduce(const float *partial, const int32_t *ranges, int nelem, int k3, float *dw,
                                   cudaStream_t s) {
-    LAT_CUDA_TRY(launch_pdl(wq8::wgrad_q8_reduce_kernel, dim3(unsigned((nelem + 127) / 128), unsigned(k3)),
+    LAT_CUDA_TRY(launch_pdl(wq8::wgrad_q8_reduce_kernel, dim3(unsigned((nelem + 255) / 256), unsigned(k3)),
                             dim3(32, wq8::kRedRows), 0, s, partial, ranges, nelem, dw));
     return LAT_OK;
 }
 
 size_t wgrad_q8_tc_ws_bytes(int cin, int cout, const lat_kmap *map) {
     Carver cv(nullptr);
-    cv.take<float>(size_t(wq8::kWorkers + map->k3) * cin * cout);
+    cv.take<float>(size_t(wq8::kWorkers * wq8::kTurns + map->k3) * cin * cout);
     cv.take<int32_t>(64);
     return align_up(cv.used, 256);
 }

@@ -371,6 +371,29 @@ def test_weight_gradient_of_long_shares(cin, cout, dtype):
         _within(dw[k], ref, (2048 + 64) * 2.0 ** -23 * mag, f"offset {k}")
 
 
+@pytest.mark.parametrize("n", [64, 65, 4999, 30011])
+@pytest.mark.parametrize("cin,cout,dtype", [(64, 128, torch.bfloat16), (128, 64, torch.float16)])
+def test_weight_gradient_of_a_map_that_is_mostly_centre(n, cin, cout, dtype):
+    """Voxels with hardly a neighbour: blocks of consecutive rows, and an offset that every worker has several shares of."""
+    coords = rand_coords(np.random.default_rng(n), n, -120, 120)
+    km, nbr = _subm(coords)
+    r = scv.q8_pack(_rand(n, n, cin, dtype=dtype))
+    dy = _rand(n + 1, n, cout, dtype=dtype)
+    st = scv.new_status()
+    dw = scv.conv_wgrad_q8(r, dy, km, d_status=st)
+    scv.check_status(st)
+    x, g = values_q8(r), dy.double()
+    for k in range(27):
+        j = np.nonzero(nbr[:, k] >= 0)[0]
+        i, j = torch.from_numpy(nbr[j, k].astype(np.int64)).cuda(), torch.from_numpy(j).cuda()
+        ref, mag = x[i].t() @ g[j], x[i].abs().t() @ g[j].abs()
+        _within(dw[k], ref, (len(j) + 64) * 2.0 ** -23 * mag, f"offset {k}")
+    # scales from an address that is not a multiple of 16: gathered instead
+    odd = torch.empty(r.scale.numel() + 4, dtype=torch.uint8, device="cuda")[4:].view(r.scale.shape)
+    odd.copy_(r.scale)
+    assert torch.equal(scv.conv_wgrad_q8(scv.Q8Rows(r.q, odd), dy, km), dw)
+
+
 def test_weight_gradient_wait_that_runs_out():
     """With no time to wait the kernel gives up, says so and leaves the GPU in order: the next call is right."""
     coords = rand_coords(np.random.default_rng(6), 5000, -12, 12)
