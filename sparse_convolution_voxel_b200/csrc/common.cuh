@@ -251,14 +251,22 @@ struct SideStream {
     cudaStream_t side = nullptr;
     cudaEvent_t fork_ev = nullptr, join_ev = nullptr;
 };
-inline cudaError_t side_stream(SideStream *&out) {
+// This thread's side stream of the current device, not created yet where `side` is null.
+inline cudaError_t side_stream_slot(SideStream *&out) {
     constexpr int kMaxDev = 64;
     thread_local SideStream per_dev[kMaxDev];
     int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
+    const cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= kMaxDev) return cudaErrorInvalidDevice;
-    SideStream &ss = per_dev[dev];
+    out = &per_dev[dev];
+    return cudaSuccess;
+}
+inline cudaError_t side_stream(SideStream *&out) {
+    SideStream *slot = nullptr;
+    cudaError_t e = side_stream_slot(slot);
+    if (e != cudaSuccess) return e;
+    SideStream &ss = *slot;
     if (!ss.side) {
         if ((e = cudaStreamCreateWithFlags(&ss.side, cudaStreamNonBlocking)) != cudaSuccess) return e;
         if ((e = cudaEventCreateWithFlags(&ss.fork_ev, cudaEventDisableTiming)) != cudaSuccess) return e;

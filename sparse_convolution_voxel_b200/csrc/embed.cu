@@ -6,17 +6,18 @@
 // Lookup: a gather, bound by the bytes it copies.  L lanes take a row, 8 channels each.
 //
 // Gradient: the rows are sorted by token (a stable LSD radix sort of (token, row) pairs;
-// rows without a token get the key `vocab`, behind every token), so that each token's
-// rows are one run of the sorted list.  The table's rows and the sorted rows together are
-// one path of vocab + n steps: "add the next row" while its token is the current one,
-// else "store the current token's sum and go on to the next token".  The path is cut into
-// equal shares (the cut is where sorted token + position passes the share's start, found
-// by a search of the group's lanes), each walked by one group of lanes with the sum in
-// registers.  So a token with a hundred thousand rows is spread over many shares, and
-// tokens without rows, whose gradient is zero, cost the one store that they need.  A
-// token whose run crosses a cut leaves one fp32 partial per share (head: the sum up to its
-// end in a later share, tail: the sum from its begin), and a second kernel adds them in
-// share order.  No atomics: the bits depend neither on timing nor on the GPU.
+// rows without a token get the key `vocab`, behind every token), so that each token's rows
+// are one run of the sorted list.  The list is cut into equal shares, each walked by one group
+// of lanes with the sum in registers, which is stored when the token changes.  So a token with
+// a hundred thousand rows is spread over many shares.  A token whose run crosses a cut leaves
+// one fp32 partial per share (head: the sum up to its end or over a whole share, tail: the sum
+// from its begin), and another kernel adds them in share order.  No atomics on sums: the bits
+// depend neither on timing nor on the GPU.
+//
+// Tokens without rows have gradient zero, most of the table in a step of few tokens: the sort
+// marks the tokens that it meets in a bitmap, and a kernel of its own stores the other rows.
+// Where these are many megabytes, it runs on a side stream while the sort and the sums, which
+// wait for latencies more than for bandwidth, go on.
 #include <algorithm>
 
 #include "rows.cuh"
@@ -80,7 +81,11 @@ struct Pass {
 template <typename I> struct Ids {
     const I *ids;
     int64_t vocab, pad;
+    uint32_t *present;  // bitmap of the tokens with rows
 };
+__device__ __forceinline__ void mark(uint32_t *present, uint32_t word, uint32_t bits) {
+    if (bits & ~__ldcg(present + word)) atomicOr(present + word, bits);
+}
 
 template <typename I>
 __device__ __forceinline__ uint32_t sort_key(const Pass &p, const Ids<I> &d, int64_t i, int32_t &bad) {
@@ -93,47 +98,70 @@ template <typename I, int R>
 __global__ void __launch_bounds__(kThreads) count_kernel(Pass p, Ids<I> d, int32_t *d_status) {
     pdl_enter();
     __shared__ uint32_t s_cnt[kMaxBins];
+    // Tokens of this block that are marked: a bitmap while the vocabulary fits (one word of the table's bitmap
+    // then costs a block one access; with one per distinct token 489 blocks of 1,000 tokens took 33 us, now 7),
+    // else the last token by its low bits, which keeps the frequent ones from the table's words.
+    __shared__ uint32_t s_seen[kMaxBins];
+    const bool first = !p.key_in, fits = d.vocab <= 32 * kMaxBins;
     const int bins = 1 << p.bits;
     for (int b = threadIdx.x; b < bins; b += kThreads) s_cnt[b] = 0;
+    if (first)
+        for (int b = threadIdx.x; b < kMaxBins; b += kThreads) s_seen[b] = fits ? 0u : ~0u;
     __syncthreads();
     const int64_t lo = blockIdx.x * int64_t(kThreads * R), hi = min(p.n, lo + kThreads * R);
     int32_t bad = 0;
 #pragma unroll R
-    for (int64_t i = lo + threadIdx.x; i < hi; i += kThreads)
-        atomicAdd(&s_cnt[(sort_key(p, d, i, bad) >> p.shift) & (bins - 1)], 1u);
+    for (int64_t i = lo + threadIdx.x; i < hi; i += kThreads) {
+        const uint32_t key = sort_key(p, d, i, bad);
+        atomicAdd(&s_cnt[(key >> p.shift) & (bins - 1)], 1u);
+        if (!first || key >= d.vocab) continue;
+        if (fits) {
+            if (!(s_seen[key >> 5] >> (key & 31) & 1u)) atomicOr(&s_seen[key >> 5], 1u << (key & 31));
+        } else if (s_seen[key % kMaxBins] != key) {
+            s_seen[key % kMaxBins] = key;
+            mark(d.present, key >> 5, 1u << (key & 31));
+        }
+    }
     __syncthreads();
     for (int b = threadIdx.x; b < bins; b += kThreads) p.counts[int64_t(blockIdx.x) * bins + b] = s_cnt[b];
+    if (first && fits)
+        for (int b = threadIdx.x; b < (d.vocab + 31) / 32; b += kThreads)
+            if (s_seen[b]) mark(d.present, b, s_seen[b]);
     if (bad) flag(d_status, bad);
 }
 
-// 32 digit values per block: lane row t of 32 takes a run of the tiles.
+// 8 digit values per block, 128 threads each: thread row t takes a run of the tiles.
 // (Also clears the count of open runs for the sums.)
-__global__ void __launch_bounds__(1024) tile_scan_kernel(uint32_t *__restrict__ counts, uint32_t *__restrict__ totals,
-                                                         int tiles, int bins, int32_t *__restrict__ open_count) {
+constexpr int kScanBins = 8, kScanRows = 128;
+__global__ void __launch_bounds__(kScanBins * kScanRows)
+tile_scan_kernel(uint32_t *__restrict__ counts, uint32_t *__restrict__ totals, int tiles, int bins,
+                 int32_t *__restrict__ open_count) {
     pdl_enter();
     if (blockIdx.x == 0 && threadIdx.x == 0 && threadIdx.y == 0) *open_count = 0;
-    __shared__ uint32_t s[32][33];
-    const int b = blockIdx.x * 32 + threadIdx.x;
-    const int per = (tiles + 31) / 32, lo = min(tiles, int(threadIdx.y) * per), hi = min(tiles, lo + per);
+    __shared__ uint32_t s[2][kScanRows][kScanBins];
+    const int b = blockIdx.x * kScanBins + threadIdx.x, t = threadIdx.y;
+    const int per = (tiles + kScanRows - 1) / kScanRows, lo = min(tiles, t * per), hi = min(tiles, lo + per);
     uint32_t sum = 0;
     if (b < bins) {
-#pragma unroll 8
-        for (int t = lo; t < hi; ++t) sum += counts[int64_t(t) * bins + b];
+#pragma unroll 4
+        for (int i = lo; i < hi; ++i) sum += counts[int64_t(i) * bins + b];
     }
-    s[threadIdx.y][threadIdx.x] = sum;
+    uint32_t upto = sum;
+    int at = 0;
+    s[0][t][threadIdx.x] = upto;
     __syncthreads();
-    uint32_t run = 0, all = 0;
 #pragma unroll
-    for (int t = 0; t < 32; ++t) {
-        const uint32_t v = s[t][threadIdx.x];
-        if (t < int(threadIdx.y)) run += v;
-        all += v;
+    for (int m = 1; m < kScanRows; m <<= 1, at ^= 1) {
+        if (t >= m) upto += s[at][t - m][threadIdx.x];
+        s[at ^ 1][t][threadIdx.x] = upto;
+        __syncthreads();
     }
     if (b >= bins) return;
-    if (threadIdx.y == 0) totals[b] = all;
-    for (int t = lo; t < hi; ++t) {
-        const uint32_t v = counts[int64_t(t) * bins + b];
-        counts[int64_t(t) * bins + b] = run;
+    if (t == kScanRows - 1) totals[b] = upto;
+    uint32_t run = upto - sum;
+    for (int i = lo; i < hi; ++i) {
+        const uint32_t v = counts[int64_t(i) * bins + b];
+        counts[int64_t(i) * bins + b] = run;
         run += v;
     }
 }
@@ -250,6 +278,8 @@ sort_small_kernel(Ids<I> d, int n, int bits, uint32_t *__restrict__ key_out, uin
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rounds = (n + kSmallThreads - 1) / kSmallThreads, lo = warp * rounds * 32;
     if (threadIdx.x == 0) *open_count = 0;
+    for (int64_t i = threadIdx.x; i < (d.vocab + 31) / 32; i += kSmallThreads) d.present[i] = 0;
+    __syncthreads();
     uint32_t key[kSmallRounds], row[kSmallRounds];  // row: and the rank, in the upper half
     int32_t bad = 0;
 #pragma unroll
@@ -259,6 +289,7 @@ sort_small_kernel(Ids<I> d, int n, int bits, uint32_t *__restrict__ key_out, uin
             const int64_t t = token(d.ids, i, d.vocab, d.pad, bad);
             key[r] = uint32_t(t < 0 ? d.vocab : t);
             row[r] = uint32_t(i);
+            if (t >= 0) mark(d.present, key[r] >> 5, 1u << (key[r] & 31));
         }
     }
     for (int shift = 0; shift < bits; shift += kSmallBits) {
@@ -330,69 +361,28 @@ sort_small_kernel(Ids<I> d, int n, int bits, uint32_t *__restrict__ key_out, uin
 }
 
 // ------------------------------------------------------------------------ the sums
-struct Path {
+struct Runs {
     const uint32_t *key, *row;  // sorted
-    uint32_t n, vocab;          // steps: n + vocab < 2^32
-    uint32_t share;             // steps per share
+    uint32_t n, vocab;
+    uint32_t share;             // sorted rows per share
     int shares;
     int c;
     float scale;
     float *head, *tail;         // [shares][c]
-    // shares in which a run begins that goes on behind them, in any order: the share, the token,
-    // the sorted rows up to the share's end
-    int4 *open;
+    int2 *open;                 // (share, token) where a run begins that goes on behind the share, in any order
     int32_t *open_count;
+    int32_t *last;              // [vocab]: of a token whose run ends behind a cut, the share with its end
     float *dtable;
 };
 
-// One range of a search: the first index in [lo, hi) at which `before` no longer holds (hi if it
-// holds everywhere).  W lanes of a group search together: a round splits the range into W + 1
-// parts, so 500,000 rows take four dependent reads with 32 lanes.
-template <int W>
-struct Range {
-    uint32_t lo, hi;
-    __device__ __forceinline__ uint32_t part(uint32_t k) const {
-        return lo + uint32_t(uint64_t(hi - lo) * k / (W + 1));
-    }
-    // votes of the group's lanes for their probes part(lane + 1): the probes are in order, so the votes are a prefix
-    __device__ __forceinline__ void narrow(uint32_t votes) {
-        if (lo >= hi) return;
-        const int k = __popc(votes);
-        const uint32_t nlo = k == 0 ? lo : part(k) + 1, nhi = k == W ? hi : part(k + 1);
-        lo = nlo;
-        hi = nhi;
-    }
-};
-
-// Sorted rows among the first a and the first b steps of the path: the first i with
-// key[i] + i >= a (b); key[i] + i increases strictly.  The two searches share their rounds.
-// mask, first: the group's lanes in its warp.
-template <int W>
-__device__ __forceinline__ void path_rows(const Path &p, uint32_t a, uint32_t b, int lane, uint32_t mask, int first,
-                                          uint32_t &ia, uint32_t &ib) {
-    Range<W> ra{a > p.vocab ? a - p.vocab : 0u, min(a, p.n)}, rb{b > p.vocab ? b - p.vocab : 0u, min(b, p.n)};
-    auto before = [&](const Range<W> &r, uint32_t step) {
-        if (r.lo >= r.hi) return false;
-        const uint32_t at = r.part(lane + 1);
-        return uint64_t(__ldg(p.key + at)) + at < step;
-    };
-    while (ra.lo < ra.hi || rb.lo < rb.hi) {
-        const bool ba = before(ra, a), bb = before(rb, b);
-        ra.narrow((__ballot_sync(mask, ba) & mask) >> first);
-        rb.narrow((__ballot_sync(mask, bb) & mask) >> first);
-    }
-    ia = ra.lo;
-    ib = rb.lo;
-}
-
-// A group's lanes read the tokens and rows of L steps at a time, one step each, and the next
+// A group's lanes read the tokens and rows of L sorted rows at a time, one each, and the next
 // ones before they add; kFlight rows of dy are in flight while kFlight are added.  A row of
 // more than 256 channels takes several groups (slabs), up to eight of them side by side in a
 // block, so that a block reads and writes long pieces.  A block takes `per_block` consecutive
 // shares; if a token's run covers them all, their sums meet in shared memory and the first
 // share's head stands for the block.
 template <typename T, int L>
-__global__ void __launch_bounds__(kThreads, 3) sums_kernel(Path p, const T *__restrict__ dy, int per_block) {
+__global__ void __launch_bounds__(kThreads, 3) sums_kernel(Runs p, const T *__restrict__ dy, int per_block) {
     pdl_enter();
     constexpr int kFlight = sizeof(T) == 4 || L == 4 ? 2 : 4;  // an even number of times per batch
     __shared__ float s_acc[8][kThreads];
@@ -400,24 +390,23 @@ __global__ void __launch_bounds__(kThreads, 3) sums_kernel(Path p, const T *__re
     const uint32_t mask = (L == 32 ? 0xFFFFFFFFu : ((1u << (L & 31)) - 1u) << first);
     const int slabs = L < 32 ? 1 : int(blockDim.x) / L / per_block;  // of a block
     const int v = blockIdx.x * per_block + group / slabs;
-    const uint32_t steps = p.vocab + p.n;
-    const uint32_t s0 = uint32_t(min(uint64_t(v) * p.share, uint64_t(steps)));
-    const uint32_t s1 = uint32_t(min(uint64_t(s0) + p.share, uint64_t(steps)));
-    uint32_t i0, i1;
-    path_rows<L>(p, s0, s1, lane, mask, first, i0, i1);
-    const uint32_t r0 = s0 - i0, r1 = s1 - i1;
+    const uint32_t i0 = uint32_t(min(uint64_t(v) * p.share, uint64_t(p.n)));
+    const uint32_t i1 = uint32_t(min(uint64_t(i0) + p.share, uint64_t(p.n)));
     const int vi = (int(blockIdx.y) * slabs + group % slabs) * L + lane;
     const bool own = vi < p.c / 8;
     const uint32_t col = vi * 8;
-    // the first token's run began in an earlier share; the last token's run goes on in the next one
-    const bool cut = i0 > 0 && __ldg(p.key + i0 - 1) == r0;
-    const bool goes_on = r1 < p.vocab && i1 > 0 && __ldg(p.key + i1 - 1) == r1;
+    // the first token, and whether its run began in an earlier share; the last token, and whether its run goes on
+    const bool some = i0 < i1;
+    const uint32_t r0 = some ? __ldg(p.key + i0) : p.vocab, r1 = some ? __ldg(p.key + i1 - 1) : p.vocab;
+    const bool cut = some && i0 > 0 && __ldg(p.key + i0 - 1) == r0;
+    const bool goes_on = r1 < p.vocab && i1 < p.n && __ldg(p.key + i1) == r1;
     float acc[8] = {};
     uint32_t r = r0;
-    auto store = [&]() {
-        if (own) {
+    auto store = [&]() {  // the sum of token r
+        if (own && r < p.vocab) {
             if (cut && r == r0) {
                 rows::st(p.head + v * int64_t(p.c) + col, acc);
+                if (vi == 0) p.last[r] = v;
             } else {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) acc[e] *= p.scale;
@@ -426,17 +415,8 @@ __global__ void __launch_bounds__(kThreads, 3) sums_kernel(Path p, const T *__re
         }
 #pragma unroll
         for (int e = 0; e < 8; ++e) acc[e] = 0.f;
-        ++r;
     };
-    auto go_to = [&](uint32_t t) {  // the path's stores up to token t
-        if (r >= t) return;
-        store();
-        if (r >= t) return;
-        float *at = p.dtable + int64_t(r) * p.c + col;
-        for (; r < t; ++r, at += p.c)
-            if (own) rows::st(at, acc);  // tokens without rows: zeros
-    };
-    // a step past the share's end, and a row without a token, adds nothing
+    // behind the share's end, and for a row without a token, there is nothing to add
     auto step_key = [&](uint32_t i) { return i < i1 ? __ldg(p.key + i) : p.vocab; };
     auto step_row = [&](uint32_t i) { return i < i1 ? __ldg(p.row + i) : 0u; };
     uint32_t key = step_key(i0 + lane), row = step_row(i0 + lane), next_key = 0, next_row = 0;
@@ -449,12 +429,15 @@ __global__ void __launch_bounds__(kThreads, 3) sums_kernel(Path p, const T *__re
         }
     };
     load(x[0], key, row, 0);
+    uint32_t before_batch = r0;
     for (uint32_t b = i0; b < i1; b += L) {
         next_key = step_key(b + L + lane);
         next_row = step_row(b + L + lane);
-        // steps of this batch that begin a new token (bit: the step)
-        const uint32_t before = __shfl_up_sync(mask, key, 1, L);
-        const uint32_t begins = (__ballot_sync(mask, (lane == 0 || key != before) && key < p.vocab) & mask) >> first;
+        // rows of this batch (bit: the row) whose token is not the one before it
+        uint32_t before = __shfl_up_sync(mask, key, 1, L);
+        if (lane == 0) before = before_batch;
+        const uint32_t begins = (__ballot_sync(mask, key != before) & mask) >> first;
+        before_batch = __shfl_sync(mask, key, L - 1, L);
 #pragma unroll
         for (int q = 0; q < L; q += kFlight) {
             const int now = (q / kFlight) & 1;
@@ -463,7 +446,10 @@ __global__ void __launch_bounds__(kThreads, 3) sums_kernel(Path p, const T *__re
             else load(x[now ^ 1], next_key, next_row, 0);
 #pragma unroll
             for (int u = 0; u < kFlight; ++u) {
-                if ((begins >> (q + u)) & 1u) go_to(__shfl_sync(mask, key, q + u, L));
+                if (((begins >> (q + u)) & 1u) && b + q + u < i1) {
+                    store();
+                    r = __shfl_sync(mask, key, q + u, L);
+                }
                 float f[8];
                 rows::to_f(x[now][u], f);
 #pragma unroll
@@ -473,7 +459,7 @@ __global__ void __launch_bounds__(kThreads, 3) sums_kernel(Path p, const T *__re
         key = next_key;
         row = next_row;
     }
-    go_to(r1);
+    if (some && !goes_on) store();
     const bool through = cut && goes_on && r == r0;  // the share lies inside one token's run
     if (per_block > 1 && __syncthreads_and(through)) {
 #pragma unroll
@@ -487,7 +473,7 @@ __global__ void __launch_bounds__(kThreads, 3) sums_kernel(Path p, const T *__re
         }
     } else if (goes_on && own) {
         rows::st((through ? p.head : p.tail) + v * int64_t(p.c) + col, acc);
-        if (!through && vi == 0) p.open[atomicAdd(p.open_count, 1)] = make_int4(v, int(r1), int(i1), 0);
+        if (!through && vi == 0) p.open[atomicAdd(p.open_count, 1)] = make_int2(v, int(r1));
     }
 }
 
@@ -497,24 +483,15 @@ __global__ void __launch_bounds__(kThreads, 3) sums_kernel(Path p, const T *__re
 // t, t + kJoinRows, ... in order, then the rows' sums are added in order.  The list's order
 // does not matter: every token is the sum of one entry.
 constexpr int kJoinRows = 8, kJoinBlocks = 1184;
-__global__ void __launch_bounds__(32 * kJoinRows) join_kernel(Path p, int per_block) {
+__global__ void __launch_bounds__(32 * kJoinRows) join_kernel(Runs p, int per_block) {
     pdl_enter();
-    __shared__ int s_last;
     __shared__ float4 s[kJoinRows][32];
     const int count = *p.open_count;
     for (int o = blockIdx.x; o < count; o += gridDim.x) {
-        const int4 run = p.open[o];
+        const int2 run = p.open[o];
         const int v = run.x;
         const uint32_t token = uint32_t(run.y);
-        if (threadIdx.y == 0) {
-            // the first sorted row past the run
-            Range<32> r{uint32_t(run.z), p.n};
-            while (r.lo < r.hi)
-                r.narrow(__ballot_sync(0xFFFFFFFFu, __ldg(p.key + r.part(threadIdx.x + 1)) <= token));
-            if (threadIdx.x == 0) s_last = int((uint64_t(r.lo) + token) / p.share);  // the share that stores the token
-        }
-        __syncthreads();
-        const int last = s_last;
+        const int last = p.last[token];
         // shares v .. end of v's block, whole blocks, then the shares of the last block
         const int block = v / per_block, blocks = max(0, last / per_block - block - 1);
         const int lead = min(last, (block + 1) * per_block - 1) - v + 1;
@@ -548,6 +525,20 @@ __global__ void __launch_bounds__(32 * kJoinRows) join_kernel(Path p, int per_bl
     }
 }
 
+// Zeros for the tokens without rows: L lanes take a table row.
+template <int L>
+__global__ void __launch_bounds__(kThreads)
+zeros_kernel(const uint32_t *__restrict__ present, uint32_t vocab, int c, float *__restrict__ dtable) {
+    pdl_enter();
+    const float zero[8] = {};
+    const uint32_t stride = gridDim.x * (kThreads / L);
+    for (uint64_t r = blockIdx.x * (kThreads / L) + threadIdx.x / L; r < vocab; r += stride) {
+        if ((__ldg(present + (r >> 5)) >> (r & 31)) & 1u) continue;
+        float *at = dtable + int64_t(r) * c;
+        for (int vi = threadIdx.x % L; vi < c / 8; vi += L) rows::st(at + vi * 8, zero);
+    }
+}
+
 // ----------------------------------------------------------------------------- host
 // Lanes of a group for rows of c channels.
 static int lanes_of(int c) {
@@ -565,11 +556,11 @@ static lat_status by_lanes(int c, F &&f) {
     return f(std::integral_constant<int, 32>{});
 }
 
-// Shares of the path: one wave of groups (the sums' registers admit 24 warps on each of a
-// B200's 148 SMs), but at least 16 steps each; the numbers depend on the sizes alone.
-static int path_shares(int64_t n, int64_t vocab, int c) {
+// Shares of the sorted rows: one wave of groups (the sums' registers admit 24 warps on each of a
+// B200's 148 SMs), but at least 16 rows each; the numbers depend on the sizes alone.
+static int run_shares(int64_t n, int c) {
     const int64_t slabs = (c / 8 + 31) / 32, want = 148 * 24 * (32 / lanes_of(c)) / slabs;
-    return int(std::max<int64_t>(1, std::min<int64_t>(want, (n + vocab + 15) / 16)));
+    return int(std::max<int64_t>(1, std::min<int64_t>(want, (n + 15) / 16)));
 }
 
 static int key_bits(int64_t vocab) {
@@ -583,14 +574,35 @@ static int key_bits(int64_t vocab) {
 static int tile_rounds(int64_t n) { return n <= 65536 ? 2 : 4; }
 static int64_t tiles_of(int64_t n) {
     const int64_t tile = kThreads * tile_rounds(n);
-    return (n + tile - 1) / tile;
+    return std::max<int64_t>(1, (n + tile - 1) / tile);
+}
+
+// Zeros of at least this many bytes go to the side stream: a fork and a join cost a few
+// microseconds, the zeros of 16 MB as many.
+constexpr size_t kSideBytes = size_t(16) << 20;
+// Blocks of the zeros: few, so that the sort's and the sums' reads do not queue behind their writes
+// (16,383 x 1024, 50,257 tokens: 64 us; with four times as many 71, on one stream 74).
+constexpr int kZeroBlocks = 74;
+constexpr int64_t kSmallWords = 32768;  // of the bitmap that the one-block sort clears itself
+
+// The side stream, or null where there is none to be had: creating it is left to calls outside
+// a capture, and one that takes part in another stream's capture is not ours to use.
+static SideStream *free_side_stream(cudaStream_t s) {
+    cudaStreamCaptureStatus mine = cudaStreamCaptureStatusNone, its = cudaStreamCaptureStatusNone;
+    if (cudaStreamIsCapturing(s, &mine) != cudaSuccess) return nullptr;
+    SideStream *side = nullptr;
+    if (side_stream_slot(side) != cudaSuccess || (mine != cudaStreamCaptureStatusNone && !side->side)) return nullptr;
+    if (side_stream(side) != cudaSuccess || cudaStreamIsCapturing(side->side, &its) != cudaSuccess) return nullptr;
+    return its == cudaStreamCaptureStatusNone ? side : nullptr;
 }
 
 struct Ws {
     uint32_t *key[2], *row[2], *counts, *totals;
     float *head, *tail;
-    int4 *open;
+    int2 *open;
     int32_t *open_count;
+    int32_t *last;
+    uint32_t *present;
     size_t bytes;
     Ws(void *base, int64_t n, int64_t vocab, int c) {
         Carver cv(base);
@@ -600,11 +612,13 @@ struct Ws {
         }
         counts = cv.take<uint32_t>(size_t(tiles_of(n)) * kMaxBins);
         totals = cv.take<uint32_t>(kMaxBins);
-        const size_t part = size_t(path_shares(n, vocab, c)) * size_t(c);
+        const size_t part = size_t(run_shares(n, c)) * size_t(c);
         head = cv.take<float>(part);
         tail = cv.take<float>(part);
-        open = cv.take<int4>(size_t(path_shares(n, vocab, c)));
+        open = cv.take<int2>(size_t(run_shares(n, c)));
         open_count = cv.take<int32_t>(1);
+        last = cv.take<int32_t>(size_t(vocab));
+        present = cv.take<uint32_t>(size_t(vocab + 31) / 32);
         bytes = align_up(cv.used, 256);
     }
 };
@@ -613,45 +627,75 @@ template <typename T, typename I>
 lat_status wgrad(const I *ids, int64_t n, const T *dy, int64_t vocab, int c, float scale, int64_t pad, float *dtable,
                  void *ws, int32_t *d_status, cudaStream_t s) {
     Ws w(ws, n, vocab, c);
+    const int64_t words = (vocab + 31) / 32;
+    const Ids<I> d{ids, vocab, pad, w.present};
+    SideStream *side = nullptr;  // where the zeros go, if not to s
+    auto zeros = [&](cudaStream_t to) -> lat_status {
+        return by_lanes(c, [&](auto l) -> lat_status {
+            constexpr int L = decltype(l)::value;
+            const int64_t blocks = std::min<int64_t>((vocab + kThreads / L - 1) / (kThreads / L), kZeroBlocks);
+            LAT_CUDA_TRY(launch_pdl(zeros_kernel<L>, dim3(unsigned(blocks)), dim3(kThreads), 0, to, w.present,
+                                    uint32_t(vocab), c, dtable));
+            return LAT_OK;
+        });
+    };
+    auto fork_zeros = [&]() -> lat_status {  // the bitmap is complete on s
+        if (size_t(vocab) * size_t(c) * sizeof(float) >= kSideBytes) side = free_side_stream(s);
+        if (!side) return zeros(s);
+        LAT_CUDA_TRY(side_fork(*side, s));
+        return zeros(side->side);
+    };
     int at = 0;
-    if (n > 0 && n <= kSmall) {
+    if (n <= kSmall && words <= kSmallWords) {
         auto kern = sort_small_kernel<I>;
         LAT_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kSmallSmem)));
-        LAT_CUDA_TRY(launch_pdl(kern, dim3(1), dim3(kSmallThreads), kSmallSmem, s, Ids<I>{ids, vocab, pad}, int(n),
-                                key_bits(vocab), w.key[0], w.row[0], w.open_count, d_status));
-    } else if (n > 0) {
-        const int bits = key_bits(vocab), passes = (bits + kMaxBits - 1) / kMaxBits, digit = std::max(2, (bits + passes - 1) / passes);
-        const int tiles = int(tiles_of(n)), bins = 1 << digit;
+        LAT_CUDA_TRY(launch_pdl(kern, dim3(1), dim3(kSmallThreads), kSmallSmem, s, d, int(n), key_bits(vocab), w.key[0],
+                                w.row[0], w.open_count, d_status));
+        const lat_status st = fork_zeros();
+        if (st != LAT_OK) return st;
+    } else {
+        LAT_CUDA_TRY(fill_u32(w.present, words, 0u, s));
+        const int bits = key_bits(vocab), passes = (bits + kMaxBits - 1) / kMaxBits;
+        const int digit = std::max(2, (bits + passes - 1) / passes), tiles = int(tiles_of(n));
+        const int bins = 1 << digit;
         const bool few = tile_rounds(n) == 2;
         auto count = few ? count_kernel<I, 2> : count_kernel<I, 4>;
         auto scatter = few ? scatter_kernel<I, 2> : scatter_kernel<I, 4>;
-        const Ids<I> d{ids, vocab, pad};
         for (int i = 0; i < passes; ++i) {
             const int to = i & 1;
             Pass p{i ? w.key[1 - to] : nullptr, i ? w.row[1 - to] : nullptr, w.key[to], w.row[to], w.counts, w.totals, n,
                    tiles, i * digit, digit};
             LAT_CUDA_TRY(launch_pdl(count, dim3(tiles), dim3(kThreads), 0, s, p, d, i ? nullptr : d_status));
-            LAT_CUDA_TRY(launch_pdl(tile_scan_kernel, dim3((bins + 31) / 32), dim3(32, 32), 0, s, w.counts, w.totals,
+            if (i == 0) {
+                const lat_status st = fork_zeros();
+                if (st != LAT_OK) return st;
+            }
+            LAT_CUDA_TRY(launch_pdl(tile_scan_kernel, dim3((bins + kScanBins - 1) / kScanBins), dim3(kScanBins, kScanRows), 0, s, w.counts, w.totals,
                                     tiles, bins, w.open_count));
             LAT_CUDA_TRY(launch_pdl(scatter, dim3(tiles), dim3(kThreads), 0, s, p, d));
             at = to;
         }
     }
-    Path p{w.key[at], w.row[at], uint32_t(n), uint32_t(vocab), 0, path_shares(n, vocab, c), c, scale, w.head, w.tail,
-           w.open, w.open_count, dtable};
-    p.share = uint32_t((n + vocab + p.shares - 1) / p.shares);
-    const int groups = kThreads / lanes_of(c), slabs = (c / 8 + 31) / 32, side = std::min(slabs, groups);
-    const int per_block = groups / side;
-    const lat_status st = by_lanes(c, [&](auto l) -> lat_status {
-        constexpr int L = decltype(l)::value;
-        const dim3 grid(unsigned((p.shares + per_block - 1) / per_block), unsigned((slabs + side - 1) / side));
-        LAT_CUDA_TRY(launch_pdl(sums_kernel<T, L>, grid, dim3(unsigned(L * side * per_block)), 0, s, p, dy, per_block));
-        return LAT_OK;
-    });
-    if (st != LAT_OK || n == 0) return st;
-    const int cols = (c + 127) / 128;
-    LAT_CUDA_TRY(launch_pdl(join_kernel, dim3(unsigned(std::min(p.shares, std::max(1, kJoinBlocks / cols))), unsigned(cols)),
-                            dim3(32, kJoinRows), 0, s, p, per_block));
+    if (n > 0) {
+        Runs p{w.key[at], w.row[at], uint32_t(n), uint32_t(vocab), 0, run_shares(n, c), c, scale, w.head, w.tail, w.open,
+               w.open_count, w.last, dtable};
+        p.share = uint32_t((n + p.shares - 1) / p.shares);
+        const int groups = kThreads / lanes_of(c), slabs = (c / 8 + 31) / 32, beside = std::min(slabs, groups);
+        const int per_block = groups / beside;
+        const lat_status st = by_lanes(c, [&](auto l) -> lat_status {
+            constexpr int L = decltype(l)::value;
+            const dim3 grid(unsigned((p.shares + per_block - 1) / per_block), unsigned((slabs + beside - 1) / beside));
+            LAT_CUDA_TRY(launch_pdl(sums_kernel<T, L>, grid, dim3(unsigned(L * beside * per_block)), 0, s, p, dy,
+                                    per_block));
+            return LAT_OK;
+        });
+        if (st != LAT_OK) return st;
+        const int cols = (c + 127) / 128;
+        LAT_CUDA_TRY(launch_pdl(join_kernel,
+                                dim3(unsigned(std::min(p.shares, std::max(1, kJoinBlocks / cols))), unsigned(cols)),
+                                dim3(32, kJoinRows), 0, s, p, per_block));
+    }
+    if (side) LAT_CUDA_TRY(side_join(*side, s));
     return LAT_OK;
 }
 

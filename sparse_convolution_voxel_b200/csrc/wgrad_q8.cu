@@ -511,7 +511,7 @@ wgrad_q8_kernel(const __grid_constant__ CUtensorMap dy_map, int centre, const ui
 // float4 columns of dW[k], two per thread; row r of kRedRows adds the slots first + r,
 // first + r + kRedRows, ... in order, then the rows' sums are added in order.  Offsets
 // without pairs get 0.
-constexpr int kRedRows = 8;
+constexpr int kRedRows = 16;
 __global__ void __launch_bounds__(32 * kRedRows)
 wgrad_q8_reduce_kernel(const float *__restrict__ partial, const int32_t *__restrict__ ranges, int nelem,
                        float *__restrict__ dw) {
@@ -528,7 +528,7 @@ wgrad_q8_reduce_kernel(const float *__restrict__ partial, const int32_t *__restr
         a.z += x.z;
         a.w += x.w;
     };
-#pragma unroll 4
+#pragma unroll 5
     for (int v = v0 + int(threadIdx.y); v <= v1; v += kRedRows) {
         const float *src = partial + int64_t(v) * nelem + el;
 #pragma unroll

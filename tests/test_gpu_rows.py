@@ -6,6 +6,8 @@ terms in fp32, in any order, is off by at most (m - 1) 2^-24 times the sum of th
 its own error plus e4m3's half step, 2^-4 of the value, or 2^-10 of the scale, which is below
 2 amax / 448 (and at least 2^-126).
 """
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -529,6 +531,31 @@ def test_a_step_on_another_stream_and_captured():
     for _, outs in graphs:
         for a, b in zip(outs, want):
             assert torch.equal(a, b)
+
+
+def test_lookup_gradient_of_a_large_table_captured():
+    """Zeros of many megabytes take the side stream, inside a capture too, and in a thread whose first call is captured."""
+    ids, dy = _ids(3, 9000, 40000, torch.int64), _rand(4, 9000, 128, dtype=torch.bfloat16)
+    want = scv.embed_wgrad(ids, dy, 40000)
+    ws = scv.Workspace()
+    out = scv.embed_wgrad(ids, dy, 40000, ws=ws).fill_(float("nan"))
+
+    def captured(got):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=torch.cuda.Stream()):
+            scv.embed_wgrad(ids, dy, 40000, ws=ws, out=out)
+        for _ in range(2):
+            out.fill_(float("nan"))
+            g.replay()
+            torch.cuda.synchronize()
+            got.append(out.clone())
+
+    got = []
+    captured(got)
+    thread = threading.Thread(target=captured, args=(got,))
+    thread.start()
+    thread.join()
+    assert len(got) == 4 and all(torch.equal(o, want) for o in got)
 
 
 def test_two_streams_at_once():
