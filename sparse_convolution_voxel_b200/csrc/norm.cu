@@ -136,7 +136,7 @@ template <typename T> struct Bwd {
 // Rows in the ring (the one at work included): what 200 KB of shared memory per SM admit.
 template <typename T, int L, int K>
 constexpr int ring_rows() {
-    return K == 4 ? (sizeof(T) == 4 ? 1 : 2) : sizeof(T) == 4 ? 2 : K == 2 && L == 0 ? 3 : 4;
+    return K == 4 && sizeof(T) == 4 ? 1 : K == 4 || sizeof(T) == 4 || (K == 2 && L == 0) ? 2 : 4;
 }
 // Bytes of a thread's slices of one row.
 template <typename T, int K, bool Q8>
@@ -145,7 +145,8 @@ constexpr int ring_bytes(bool dh) {
 }
 
 template <typename T, int L, int K, bool Q8>
-__global__ void __launch_bounds__(L == 0 ? kWideThreads : kThreads, L > 0 && K == 1 ? 4 : 1) norm_bwd_kernel(Bwd<T> a) {
+__global__ void __launch_bounds__(L == 0 ? kWideThreads : kThreads, L > 0 && K == 1 ? 4 : L == 0 && K == 2 && sizeof(T) == 2 ? 2 : 1)
+norm_bwd_kernel(Bwd<T> a) {
     pdl_enter();
     __shared__ float s_sum[2 * kMaxWarps];
     extern __shared__ __align__(16) uint8_t s_ring[];  // and, at the end, the groups' sums of dw: [kThreads / L][c]
@@ -391,7 +392,7 @@ static int rows_per_block(int c) {
 
 // Blocks of the backward pass: as many as fit a B200's 148 SMs at once, by the ring.
 static int64_t shares(int64_t n, int c) {
-    const int64_t per = rows_per_block(c), most = c <= 256 ? 592 : c <= 512 ? 296 : c <= 1024 ? 592 : c <= 8192 ? 296 : 148;
+    const int64_t per = rows_per_block(c), most = c <= 256 ? 592 : c <= 512 ? 296 : c <= 1024 ? 592 : c <= 8192 ? 444 : 148;
     return std::max<int64_t>(1, std::min<int64_t>(most, (n + per - 1) / per));
 }
 
