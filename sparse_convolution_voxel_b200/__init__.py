@@ -290,10 +290,19 @@ def _on(stream, device):
     return torch.cuda.stream(torch.cuda.ExternalStream(stream, device) if isinstance(stream, int) else stream)
 
 
+def _rows_like(x, n: int, c: int, dtype):
+    """An (n, c) tensor beside x (empty_strided: half the time of empty, which counts for a few rows)."""
+    return torch.empty_strided((n, c), (c, 1), dtype=dtype, device=x.device)
+
+
+def _vector_like(x, n: int):
+    return torch.empty_strided((n,), (1,), dtype=torch.float32, device=x.device)
+
+
 def embed_fwd(ids, table, scale: float = 1.0, pad_id: int = -1, d_status=None, out=None, stream=None):
     """scale * table[ids] (n, c); rows whose id is pad_id are 0.  ids int32 or int64 (n,)."""
     with _on(stream, table.device):
-        y = out if out is not None else table.new_empty((ids.shape[0], table.shape[1]))
+        y = out if out is not None else _rows_like(table, ids.shape[0], table.shape[1], table.dtype)
         lat_embed_fwd(ids, table, scale, pad_id, y, d_status, stream)
     return y
 
@@ -302,7 +311,7 @@ def embed_wgrad(ids, dy, vocab: int, scale: float = 1.0, pad_id: int = -1, ws: W
                 out=None, stream=None):
     """The table's gradient (vocab, c) in fp32: scale * the sum of dy's rows of each token."""
     with _on(stream, dy.device):
-        dt = out if out is not None else dy.new_empty((vocab, dy.shape[1]), dtype=torch.float32)
+        dt = out if out is not None else _rows_like(dy, vocab, dy.shape[1], torch.float32)
         if dt.shape[0] != vocab:
             raise ValueError(f"out has {dt.shape[0]} rows, not {vocab}")
         ws = ws or Workspace(dy.device)
@@ -329,8 +338,8 @@ class Q8Rows:
     def like(cls, x: torch.Tensor) -> "Q8Rows":
         """Room for the rows of x."""
         n, c = x.shape
-        return cls(x.new_empty((n, c), dtype=torch.float8_e4m3fn),
-                   x.new_empty((n, -(-c // LAT_Q8_GROUP)), dtype=torch.uint8))
+        return cls(torch.empty_like(x, dtype=torch.float8_e4m3fn),
+                   _rows_like(x, n, -(-c // LAT_Q8_GROUP), torch.uint8))
 
     @property
     def shape(self):
@@ -381,7 +390,7 @@ def rms_norm_fwd(x, w=None, res=None, eps: float = 1e-6, rows: bool = True, q8: 
     with _on(stream, x.device):
         h = h_out if h_out is not None else torch.empty_like(x) if res is not None else None
         y = torch.empty_like(x) if rows else None
-        rstd = x.new_empty(x.shape[:1], dtype=torch.float32)
+        rstd = _vector_like(x, x.shape[0])
         y8 = Q8Rows.like(x) if q8 else None
         h8 = Q8Rows.like(x) if q8_h else None
         lat_rms_norm_fwd(x, res, w, eps, h, y, y8.q if q8 else None, y8.scale if q8 else None, h8.q if q8_h else None,
@@ -394,7 +403,7 @@ def rms_norm_bwd(dy, h, rstd, w=None, dh=None, want_dw: bool = True, ws: Workspa
     alike, with dh (the gradient that reaches h past the norm) added; dw in fp32, None without ``want_dw``."""
     with _on(stream, dy.device):
         dx = out if out is not None else torch.empty_like(dy)
-        dw = dy.new_empty(dy.shape[1:], dtype=torch.float32) if want_dw else None
+        dw = _vector_like(dy, dy.shape[1]) if want_dw else None
         buf = None
         if want_dw:
             ws = ws or Workspace(dy.device)
