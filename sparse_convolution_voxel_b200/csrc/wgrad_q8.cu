@@ -14,7 +14,8 @@
 //     and a ring of kRing blocks (raw x rows, scale bytes, dy tile) of its own: wait for the
 //     block's copies, widen x into an A tile, arrive at the tile's barrier.  (One group took
 //     95 us at 500k rows, 128 -> 128: a chain of latencies in two warps per scheduler.)
-//   * four warps gather the blocks' rows with cp.async, dy straight into its swizzled tile.
+//   * four warps per group gather the blocks' rows with cp.async, dy straight into its
+//     swizzled tile.
 //   * one thread fetches the blocks that are a run: three quarters of a scan's pairs are
 //     (j, j), the centre of a submanifold map, in row order, so that 64 pairs are 64
 //     consecutive rows: bulk copies of x and the scales, a tensor copy per 64 channels of dy.
@@ -44,15 +45,16 @@ constexpr int kKP = 64;        // pairs per block (GEMM K block)
 // workers: in one share each, the CTAs with gathers alone took 77 us and the others 53.
 constexpr int kWorkers = 148, kTurns = 4;
 constexpr int kGroups = 2, kGroupWarps = 8;
-constexpr int kWideWarps = kGroups * kGroupWarps, kEpiWarps = 4, kGatherWarps = 4;
+constexpr int kWideWarps = kGroups * kGroupWarps, kEpiWarps = 4, kGatherWarps = 4;  // gathering: per group
 constexpr int kGroupThreads = kGroupWarps * 32, kGatherThreads = kGatherWarps * 32;
 constexpr int kRing = 3;      // blocks in a group's ring
 constexpr int kTiles = 2;     // A tiles of a group
+static_assert(kRing == kTiles + 1, "the block whose MMAs free the A tile has the next ring slot");
 constexpr int kFlush = 32;    // blocks per accumulator
-constexpr int kLook = 4;      // blocks whose pairs are read ahead
+constexpr int kLook = 3;      // blocks of a group whose pairs are read ahead
 constexpr int kScaleBytes = kKP * 4 + 32;  // of a ring slot: a word per pair, or a run's bytes from a 16-byte boundary
 constexpr int kGatherAt = kWideWarps + kEpiWarps;  // first gathering warp
-constexpr int kMmaWarp = kGatherAt + kGatherWarps, kLoadWarp = kMmaWarp + 1;
+constexpr int kMmaWarp = kGatherAt + kGroups * kGatherWarps, kLoadWarp = kMmaWarp + 1;
 constexpr int kThreads = (kLoadWarp + 1) * 32;
 constexpr int kWidePairs = kKP / kGroupWarps, kGatherPairs = kKP / kGatherWarps;  // of a block, per warp
 constexpr uint64_t kDrainNs = 1000000000ull;  // limit of the waits that drain a CTA that gave up
@@ -187,8 +189,7 @@ wgrad_q8_kernel(const __grid_constant__ CUtensorMap dy_map, int centre, const ui
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::kBars);
-    uint64_t *empty = full + kGroups * kTiles;    // A tiles
-    uint64_t *freed = empty + kGroups * kTiles;   // ring slots
+    uint64_t *freed = full + kGroups * kTiles;  // the MMAs of the slot's block are done: slot and A tile are free
     uint64_t *accfull = freed + kGroups * kRing;
     uint64_t *accempty = accfull + 2;
     uint64_t *landed = accempty + 2;  // bulk and tensor copies, [group][slot]
@@ -203,10 +204,7 @@ wgrad_q8_kernel(const __grid_constant__ CUtensorMap dy_map, int centre, const ui
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (warp == 1) s_work.make(pair_off, capacity, k3, int(blockIdx.x), blockIdx.x == 0 ? ranges : nullptr);
     if (tid == 0) {
-        for (int s = 0; s < kGroups * kTiles; ++s) {
-            ptx::mbar_init(&full[s], kGroupThreads);
-            ptx::mbar_init(&empty[s], 1);
-        }
+        for (int s = 0; s < kGroups * kTiles; ++s) ptx::mbar_init(&full[s], kGroupThreads);
         for (int s = 0; s < 2; ++s) {
             ptx::mbar_init(&accfull[s], 1);
             ptx::mbar_init(&accempty[s], kEpiWarps * 32);
@@ -249,9 +247,11 @@ wgrad_q8_kernel(const __grid_constant__ CUtensorMap dy_map, int centre, const ui
 #pragma unroll 1
         for (uint32_t it = 0; it < blocks; ++it) {
             const uint32_t r = grp * kRing + slot, t = grp * kTiles + it % kTiles;
-            // this block's copies, and the MMAs that read the A tile last
+            // this block's copies, and the MMAs that read the A tile last: of the block kTiles before, whose slot is
+            // the one after this in the ring (kRing = kTiles + 1)
+            const uint32_t was = slot + 1 == kRing ? 0 : slot + 1, was_phase = slot + 1 == kRing ? phase : phase ^ 1;
             if (!__all_sync(0xFFFFFFFFu, ptx::mbar_wait(&landed[r], phase, wait_ns) &&
-                                             ptx::mbar_wait(&empty[t], ((it / kTiles) & 1) ^ 1, wait_ns))) {
+                                             (it < kTiles || ptx::mbar_wait(&freed[grp * kRing + was], was_phase, wait_ns)))) {
                 ok = false;
                 break;
             }
@@ -330,17 +330,20 @@ wgrad_q8_kernel(const __grid_constant__ CUtensorMap dy_map, int centre, const ui
     } else if (warp < kMmaWarp) {
         // ------------------------------------------------------------ gather rows
         constexpr int XL = M / 16, XP = 32 / XL;
-        const int gw = warp - kGatherAt, xc = lane % XL, xg = lane / XL, g = lane >> 3, c = lane & 7;
+        const int grp = (warp - kGatherAt) / kGatherWarps, gw = (warp - kGatherAt) % kGatherWarps;
+        const int xc = lane % XL, xg = lane / XL, g = lane >> 3, c = lane & 7;
         Blocks<M / 32> blk(s_work, centre, n_in);
-        // lanes 0..15: the indices of this warp's pairs of the next kLook blocks (a run needs none), so that their
-        // own latency, as long as a block's work, is not met once per block
+        // lanes 0..15: the indices of this warp's pairs of the group's next kLook blocks (a run needs none), so that
+        // their own latency, as long as a block's work, is not met once per block
         int si[kLook], sj[kLook];
         bool have[kLook], run[kLook];
-        auto fetch = [&](int u) {
+        bool more = true;
+        auto fetch = [&](int u, int skip) {
             si[u] = sj[u] = -1;
-            have[u] = blk.next();
+            for (int i = 0; i < skip; ++i) more = more && blk.next();
+            have[u] = more;
             run[u] = blk.run;
-            if (!have[u] || run[u]) return;
+            if (!more || run[u]) return;
             const int64_t mp = blk.p0 + gw * kGatherPairs + lane;
             if (lane < kGatherPairs && mp < blk.hi) {
                 si[u] = __ldg(pair_in + mp);
@@ -348,12 +351,11 @@ wgrad_q8_kernel(const __grid_constant__ CUtensorMap dy_map, int centre, const ui
             }
         };
 #pragma unroll
-        for (int u = 0; u < kLook; ++u) {
-            have[u] = false;
-            if (u == 0 || have[u - 1]) fetch(u);
-        }
+        for (int u = 0; u < kLook; ++u) fetch(u, u == 0 ? 1 + grp : kGroups);
         bool ok = true;
-        uint32_t grp = 0, slot = 0, phase = 1;  // the wait for the slot's previous block; the first ones pass
+        uint32_t slot = 0, phase = 1;  // the wait for the slot's previous block; the first ones pass
+        const uint8_t *q_lane = q + xc * 16;
+        const T *dy_lane = dy + c * 8;
         auto gather = [&](int u) -> bool {
             const uint32_t r = grp * kRing + slot;
             if (!__all_sync(0xFFFFFFFFu, ptx::mbar_wait(&freed[r], phase, wait_ns))) return false;
@@ -363,7 +365,8 @@ wgrad_q8_kernel(const __grid_constant__ CUtensorMap dy_map, int centre, const ui
                     bad |= LAT_ERR_BAD_MAP;
                     ri = rj = -1;
                 }
-                uint8_t *xs = smem + C::kRawAt + r * C::kXBytes, *Bs = smem + C::kDyAt + r * C::kBBytes;
+                uint8_t *xs = smem + C::kRawAt + r * C::kXBytes + (gw * kGatherPairs + xg) * M + xc * 16;
+                uint8_t *Bs = smem + C::kDyAt + r * C::kBBytes + gw * (kGatherPairs * 128);
                 if (lane < kGatherPairs) {
                     const int p = gw * kGatherPairs + lane;
                     const int64_t at = ri < 0 ? 0 : int64_t(ri) * (M / 32), word = at & ~int64_t(3);
@@ -374,28 +377,24 @@ wgrad_q8_kernel(const __grid_constant__ CUtensorMap dy_map, int centre, const ui
                 }
 #pragma unroll
                 for (int i = 0; i < kGatherPairs / XP; ++i) {
-                    const int pl = i * XP + xg, ii = __shfl_sync(0xFFFFFFFFu, ri, pl);
-                    const uint8_t *src = ii >= 0 ? q + int64_t(ii) * M + xc * 16 : q;
-                    ptx::cp_async16(xs + (gw * kGatherPairs + pl) * M + xc * 16, src, ii >= 0 ? 16u : 0u);
+                    const int ii = __shfl_sync(0xFFFFFFFFu, ri, i * XP + xg);
+                    ptx::cp_async16(xs + i * XP * M, q_lane + uint64_t(uint32_t(max(ii, 0))) * M, ii >= 0 ? 16u : 0u);
                 }
 #pragma unroll
                 for (int i = 0; i < kGatherPairs / 4; ++i) {
-                    const int pl = 4 * i + g, p = gw * kGatherPairs + pl;
+                    const int pl = 4 * i + g;  // gw * 16 is a multiple of 8: the pair's place in its 8-pair atom is pl & 7
                     const int jj = __shfl_sync(0xFFFFFFFFu, rj, pl);
-                    const uint32_t off = (p >> 3) * 1024 + (p & 7) * 128 + ((c ^ (p & 7)) << 4);
-                    const T *src = jj >= 0 ? dy + int64_t(jj) * N + c * 8 : dy;
+                    const uint32_t off = (pl >> 3) * 1024 + (pl & 7) * 128 + ((c ^ (pl & 7)) << 4);
+                    const T *src = dy_lane + uint64_t(uint32_t(max(jj, 0))) * N;
 #pragma unroll
                     for (int nb = 0; nb < N / 64; ++nb)
-                        ptx::cp_async16(Bs + nb * 8192 + off, src + (jj >= 0 ? nb * 64 : 0), jj >= 0 ? 16u : 0u);
+                        ptx::cp_async16(Bs + nb * 8192 + off, src + nb * 64, jj >= 0 ? 16u : 0u);
                 }
             }
             ptx::cp_async_arrive_noinc(&landed[r]);  // when this thread's copies are there
-            if (++grp == kGroups) {
-                grp = 0;
-                if (++slot == kRing) {
-                    slot = 0;
-                    phase ^= 1;
-                }
+            if (++slot == kRing) {
+                slot = 0;
+                phase ^= 1;
             }
             return true;
         };
@@ -406,53 +405,55 @@ wgrad_q8_kernel(const __grid_constant__ CUtensorMap dy_map, int centre, const ui
                 if (!have[u]) break;
                 ok = gather(u);
                 if (!ok) break;
-                fetch(u);
+                fetch(u, kGroups);
             }
         }
         ptx::cp_async_wait<0>();
         if (!ok) s_abort = 1;
     } else if (warp == kMmaWarp && lane == 0) {
         // ------------------------------------------------------------ MMA issue
-        uint32_t it = 0, ta = 0;
+        // (This thread's instructions per block bound a map whose rows lie in L2: descriptors advance, nothing is divided.)
+        const uint64_t a_desc = ptx::desc_sw128(ptx::smem_u32(smem), 8192, 1024);
+        const uint64_t b_desc = ptx::desc_sw128(ptx::smem_u32(smem + C::kDyAt), 8192, 1024);
+        uint32_t grp = 0, tile = 0, slot = 0, tile_phase = 0;  // of the block; phase of its tile's barrier
+        uint32_t a = 0, a_phase = 1;                           // accumulator; the first waits pass
         bool ok = true;
         for (int i = 0; ok && i < s_work.count; ++i) {
-            const int64_t lo = s_work.seg[i].lo, hi = s_work.seg[i].hi;
-            uint32_t acc = 0, dcol = 0, a = 0;  // blocks in the accumulator
-            for (int64_t p0 = lo; p0 < hi; p0 += kKP) {
+            int left = int((s_work.seg[i].hi - s_work.seg[i].lo + kKP - 1) / kKP);
+            uint32_t acc = 0;  // blocks in the accumulator
+            for (; left > 0; --left) {
                 if (acc == 0) {
-                    a = ta & 1;
-                    if (!ptx::mbar_wait(&accempty[a], ((ta >> 1) & 1) ^ 1, wait_ns)) {
+                    if (!ptx::mbar_wait(&accempty[a], a_phase, wait_ns)) {
                         ok = false;
                         break;
                     }
                     ptx::tc_fence_after();
-                    dcol = tmem_base + a * N;
                 }
-                const uint32_t grp = it % kGroups, n = it / kGroups;  // block n of its group
-                const uint32_t t = grp * kTiles + n % kTiles, r = grp * kRing + n % kRing;
+                const uint32_t t = grp * kTiles + tile, r = grp * kRing + slot;
                 // the widened tile; its threads have seen the dy tile land
-                if (!ptx::mbar_wait(&full[t], (n / kTiles) & 1, wait_ns)) {
+                if (!ptx::mbar_wait(&full[t], tile_phase, wait_ns)) {
                     ok = false;
                     break;
                 }
                 ptx::tc_fence_after();
                 // the gathered dy rows were written by cp.async (generic proxy)
                 ptx::fence_proxy_async_smem();
-                const uint32_t as = ptx::smem_u32(smem + t * C::kABytes);
-                const uint32_t bs = ptx::smem_u32(smem + C::kDyAt + r * C::kBBytes);
+                const uint64_t ad = a_desc + t * (C::kABytes >> 4), bd = b_desc + r * (C::kBBytes >> 4);
 #pragma unroll
-                for (int ks = 0; ks < 4; ++ks) {
-                    const uint64_t ad = ptx::desc_sw128(as + ks * 2048, 8192, 1024);
-                    const uint64_t bd = ptx::desc_sw128(bs + ks * 2048, 8192, 1024);
-                    ptx::umma_f16(dcol, ad, bd, idesc, acc > 0 || ks > 0);
-                }
-                ptx::umma_commit(&empty[t]);
+                for (int ks = 0; ks < 4; ++ks)
+                    ptx::umma_f16(tmem_base + a * N, ad + ks * 128, bd + ks * 128, idesc, acc > 0 || ks > 0);
                 ptx::umma_commit(&freed[r]);
-                ++it;
-                if (++acc == kFlush || p0 + kKP >= hi) {
+                if (++acc == kFlush || left == 1) {
                     ptx::umma_commit(&accfull[a]);
-                    ++ta;
+                    a ^= 1;
+                    a_phase ^= a == 0;
                     acc = 0;
+                }
+                if (++grp == kGroups) {
+                    grp = 0;
+                    slot = slot + 1 == kRing ? 0 : slot + 1;
+                    tile ^= 1;
+                    tile_phase ^= tile == 0;
                 }
             }
         }
