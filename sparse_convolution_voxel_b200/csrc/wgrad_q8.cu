@@ -47,9 +47,8 @@ constexpr int kWorkers = 148, kTurns = 4;
 constexpr int kGroups = 2, kGroupWarps = 8;
 constexpr int kWideWarps = kGroups * kGroupWarps, kEpiWarps = 4, kGatherWarps = 4;  // gathering: per group
 constexpr int kGroupThreads = kGroupWarps * 32, kGatherThreads = kGatherWarps * 32;
-constexpr int kRing = 3;      // blocks in a group's ring
 constexpr int kTiles = 2;     // A tiles of a group
-static_assert(kRing == kTiles + 1, "the block whose MMAs free the A tile has the next ring slot");
+constexpr int kMaxRing = 8;
 constexpr int kFlush = 32;    // blocks per accumulator
 constexpr int kLook = 3;      // blocks of a group whose pairs are read ahead
 constexpr int kScaleBytes = kKP * 4 + 32;  // of a ring slot: a word per pair, or a run's bytes from a 16-byte boundary
@@ -64,11 +63,17 @@ struct Cfg {
     static constexpr uint32_t kABytes = uint32_t(M) * 128;  // 64 pairs x M channels x 2 bytes
     static constexpr uint32_t kBBytes = uint32_t(N) * 128;
     static constexpr uint32_t kXBytes = uint32_t(M) * 64;   // raw
+    // Blocks in a group's ring: what shared memory admits.  (A block takes some 3,000 cycles from its gather to its
+    // MMAs' end: where the rows lie in L2, the ring's length bounds the rate.)
+    static constexpr uint32_t kSlot = kBBytes + kXBytes + kScaleBytes;
+    static constexpr uint32_t kRoom = 232448 - 2048 - 1536 - kGroups * kTiles * kABytes;  // but static variables and barriers
+    static constexpr int kRing = kRoom / (kGroups * kSlot) < kMaxRing ? kRoom / (kGroups * kSlot) : kMaxRing;
+    static_assert(kRing > kTiles, "a group's ring is longer than its A tiles are many");
     static constexpr uint32_t kDyAt = kGroups * kTiles * kABytes;        // the A tiles, then the dy tiles, raw x, scales
     static constexpr uint32_t kRawAt = kDyAt + kGroups * kRing * kBBytes;
     static constexpr uint32_t kScaleAt = kRawAt + kGroups * kRing * kXBytes;
     static constexpr uint32_t kBars = kScaleAt + kGroups * kRing * kScaleBytes;
-    static constexpr uint32_t kSmem = kBars + 256 + 1024;
+    static constexpr uint32_t kSmem = kBars + 512 + 1024;
     static constexpr uint32_t kTmemCols = 4 * N;  // two accumulators and the total; a power of two
     static constexpr int kChunks = M / 64;  // 16-byte raw chunks per thread and block
 };
@@ -166,14 +171,36 @@ struct Blocks {
     }
 };
 
+// 16 values of a group with scale byte e, widened: lo and hi are their halves.
 template <typename T>
-__device__ __forceinline__ uint4 widen(uint2 q, int e) {
-    float v[8];
-    rows::q8_to_f(q, e, v);
+__device__ __forceinline__ void widen(const uint4 &q, int e, uint4 &lo, uint4 &hi) {
+    if constexpr (std::is_same<T, __half>::value) {
+        // scales of 2^-14 .. 2^7 are fp16 numbers and 448 of them an fp16 value: one product, rounded once
+        if (uint32_t(e - 113) < 22u) {
+            const __half2 s = __half2half2(__ushort_as_half(uint16_t((e - 112) << 10)));
+            const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+            uint32_t o[8];
 #pragma unroll
-    for (int c = 0; c < 8; ++c) v[c] = rows::in_range<T>(v[c]);
-    return make_uint4(rows::two<T>(v[0], v[1]), rows::two<T>(v[2], v[3]), rows::two<T>(v[4], v[5]),
-                      rows::two<T>(v[6], v[7]));
+            for (int i = 0; i < 8; ++i) {
+                const __half2_raw r = __nv_cvt_fp8x2_to_halfraw2(__nv_fp8x2_storage_t(w[i / 2] >> (16 * (i & 1))), __NV_E4M3);
+                const __half2 v = __hmul2(__half2(r), s);
+                o[i] = *reinterpret_cast<const uint32_t *>(&v);
+            }
+            lo = make_uint4(o[0], o[1], o[2], o[3]);
+            hi = make_uint4(o[4], o[5], o[6], o[7]);
+            return;
+        }
+    }
+    auto half = [&](uint2 w) {
+        float v[8];
+        rows::q8_to_f(w, e, v);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) v[c] = rows::in_range<T>(v[c]);
+        return make_uint4(rows::two<T>(v[0], v[1]), rows::two<T>(v[2], v[3]), rows::two<T>(v[4], v[5]),
+                          rows::two<T>(v[6], v[7]));
+    };
+    lo = half(make_uint2(q.x, q.y));
+    hi = half(make_uint2(q.z, q.w));
 }
 
 template <typename T, int M, int N>
@@ -184,6 +211,7 @@ wgrad_q8_kernel(const __grid_constant__ CUtensorMap dy_map, int centre, const ui
                 float *__restrict__ partial, int32_t *__restrict__ ranges, uint64_t wait_ns, int32_t *d_status) {
     pdl_enter();
     using C = Cfg<M, N>;
+    constexpr int kRing = C::kRing;
     constexpr uint32_t idesc = wtc::make_idesc<T, M, N>();
 
     extern __shared__ uint8_t smem_raw[];
@@ -247,9 +275,9 @@ wgrad_q8_kernel(const __grid_constant__ CUtensorMap dy_map, int centre, const ui
 #pragma unroll 1
         for (uint32_t it = 0; it < blocks; ++it) {
             const uint32_t r = grp * kRing + slot, t = grp * kTiles + it % kTiles;
-            // this block's copies, and the MMAs that read the A tile last: of the block kTiles before, whose slot is
-            // the one after this in the ring (kRing = kTiles + 1)
-            const uint32_t was = slot + 1 == kRing ? 0 : slot + 1, was_phase = slot + 1 == kRing ? phase : phase ^ 1;
+            // this block's copies, and the MMAs that read the A tile last, of the block kTiles before
+            const uint32_t was = slot >= kTiles ? slot - kTiles : slot + kRing - kTiles;
+            const uint32_t was_phase = slot >= kTiles ? phase : phase ^ 1;
             if (!__all_sync(0xFFFFFFFFu, ptx::mbar_wait(&landed[r], phase, wait_ns) &&
                                              (it < kTiles || ptx::mbar_wait(&freed[grp * kRing + was], was_phase, wait_ns)))) {
                 ok = false;
@@ -265,7 +293,8 @@ wgrad_q8_kernel(const __grid_constant__ CUtensorMap dy_map, int centre, const ui
                 const uint4 raw = *reinterpret_cast<const uint4 *>(xs + i * XP * M);
                 // channels 16 xc .. 16 xc + 15
                 const int e = ss[(from >= 0 ? from + p * (M / 32) : p * 4 + (M == 64 ? s_odd[r][p] : 0)) + (xc >> 1)];
-                const uint4 lo = widen<T>(make_uint2(raw.x, raw.y), e), hi = widen<T>(make_uint2(raw.z, raw.w), e);
+                uint4 lo, hi;
+                widen<T>(raw, e, lo, hi);
                 *reinterpret_cast<uint4 *>(row + sw * 128 + ((first ^ sw) << 4)) = turn ? hi : lo;
                 *reinterpret_cast<uint4 *>(row + sw * 128 + ((second ^ sw) << 4)) = turn ? lo : hi;
             }
