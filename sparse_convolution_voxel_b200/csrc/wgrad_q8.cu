@@ -19,8 +19,9 @@
 //   * one thread fetches the blocks that are a run: three quarters of a scan's pairs are
 //     (j, j), the centre of a submanifold map, in row order, so that 64 pairs are 64
 //     consecutive rows: bulk copies of x and the scales, a tensor copy per 64 channels of dy.
-//   * one thread issues the MMAs, whose commits free the A tile and the ring slot, and four
-//     warps store each segment's sum from TMEM.
+//   * a thread per group issues its MMAs, into an accumulator of its own; their commits free
+//     the A tile and the ring slot.  (It takes some 1,000 cycles a block: with one thread for
+//     both, that bounded maps whose rows lie in L2.)  Four warps store each segment's sum.
 // With the gathers in the widening warps, which then wait for one another's latencies, and
 // in shares of one piece, it took 76 us; now 72, of which the kernel's 66 are 5 TB/s of copies.
 //
@@ -49,11 +50,11 @@ constexpr int kWideWarps = kGroups * kGroupWarps, kEpiWarps = 4, kGatherWarps = 
 constexpr int kGroupThreads = kGroupWarps * 32, kGatherThreads = kGatherWarps * 32;
 constexpr int kTiles = 2;     // A tiles of a group
 constexpr int kMaxRing = 8;
-constexpr int kFlush = 32;    // blocks per accumulator
+constexpr int kFlush = 32;    // blocks of a group per accumulator
 constexpr int kLook = 3;      // blocks of a group whose pairs are read ahead
 constexpr int kScaleBytes = kKP * 4 + 32;  // of a ring slot: a word per pair, or a run's bytes from a 16-byte boundary
 constexpr int kGatherAt = kWideWarps + kEpiWarps;  // first gathering warp
-constexpr int kMmaWarp = kGatherAt + kGroups * kGatherWarps, kLoadWarp = kMmaWarp + 1;
+constexpr int kMmaWarp = kGatherAt + kGroups * kGatherWarps, kLoadWarp = kMmaWarp + kGroups;
 constexpr int kThreads = (kLoadWarp + 1) * 32;
 constexpr int kWidePairs = kKP / kGroupWarps, kGatherPairs = kKP / kGatherWarps;  // of a block, per warp
 constexpr uint64_t kDrainNs = 1000000000ull;  // limit of the waits that drain a CTA that gave up
@@ -74,7 +75,7 @@ struct Cfg {
     static constexpr uint32_t kScaleAt = kRawAt + kGroups * kRing * kXBytes;
     static constexpr uint32_t kBars = kScaleAt + kGroups * kRing * kScaleBytes;
     static constexpr uint32_t kSmem = kBars + 512 + 1024;
-    static constexpr uint32_t kTmemCols = 4 * N;  // two accumulators and the total; a power of two
+    static constexpr uint32_t kTmemCols = 4 * N;  // the groups' accumulators and the total; a power of two
     static constexpr int kChunks = M / 64;  // 16-byte raw chunks per thread and block
 };
 template <typename T, int M, int N> struct KernelTag {};  // one launch-config cache per kernel
@@ -219,8 +220,8 @@ wgrad_q8_kernel(const __grid_constant__ CUtensorMap dy_map, int centre, const ui
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::kBars);
     uint64_t *freed = full + kGroups * kTiles;  // the MMAs of the slot's block are done: slot and A tile are free
     uint64_t *accfull = freed + kGroups * kRing;
-    uint64_t *accempty = accfull + 2;
-    uint64_t *landed = accempty + 2;  // bulk and tensor copies, [group][slot]
+    uint64_t *accempty = accfull + kGroups;
+    uint64_t *landed = accempty + kGroups;  // bulk and tensor copies, [group][slot]
     uint64_t *drain = landed + kGroups * kRing;  // tracks the MMAs still in flight when a CTA gives up
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
     __shared__ int s_abort;
@@ -233,7 +234,7 @@ wgrad_q8_kernel(const __grid_constant__ CUtensorMap dy_map, int centre, const ui
     if (warp == 1) s_work.make(pair_off, capacity, k3, int(blockIdx.x), blockIdx.x == 0 ? ranges : nullptr);
     if (tid == 0) {
         for (int s = 0; s < kGroups * kTiles; ++s) ptx::mbar_init(&full[s], kGroupThreads);
-        for (int s = 0; s < 2; ++s) {
+        for (int s = 0; s < kGroups; ++s) {
             ptx::mbar_init(&accfull[s], 1);
             ptx::mbar_init(&accempty[s], kEpiWarps * 32);
         }
@@ -242,7 +243,7 @@ wgrad_q8_kernel(const __grid_constant__ CUtensorMap dy_map, int centre, const ui
             ptx::mbar_init(&freed[s], 1);
             s_last[s] = -1;
         }
-        ptx::mbar_init(drain, 1);
+        ptx::mbar_init(drain, kGroups);
         s_abort = 0;
         ptx::fence_mbar_init();
         ptx::fence_proxy_async_smem();
@@ -313,33 +314,48 @@ wgrad_q8_kernel(const __grid_constant__ CUtensorMap dy_map, int centre, const ui
         // M = 128: lane l of quadrant w holds row 32w + l; M = 64: lanes 0..15 hold rows 16w + l
         const int row = M == 128 ? quad * 32 + lane : quad * 16 + lane;
         const bool has_row = M == 128 || lane < 16;
-        uint32_t ta = 0;
+        uint32_t phase[kGroups] = {}, it = 0;  // it: the segment's first block
         bool ok = true;
         for (int i = 0; ok && i < s_work.count; ++i) {
             const Segment sg = s_work.seg[i];
             float *dst = partial + int64_t(sg.slot) * M * N + int64_t(row) * N;
-            for (int64_t p0 = sg.lo; p0 < sg.hi; p0 += kFlush * kKP) {
-                const bool begins = sg.begins && p0 == sg.lo, ends = sg.ends && p0 + kFlush * kKP >= sg.hi;
-                const uint32_t a = ta & 1;
-                if (!__all_sync(0xFFFFFFFFu, ptx::mbar_wait(&accfull[a], (ta >> 1) & 1, wait_ns))) {
-                    ok = false;
-                    break;
+            const int blocks = int((sg.hi - sg.lo + kKP - 1) / kKP);
+            for (int b0 = 0; b0 < blocks; b0 += kGroups * kFlush) {
+                const int n = min(kGroups * kFlush, blocks - b0);
+                const bool begins = sg.begins && b0 == 0, ends = sg.ends && b0 + n == blocks;
+                // one block alone: the other group has none
+                const bool has[kGroups] = {n > 1 || ((it + b0) & 1) == 0, n > 1 || ((it + b0) & 1) == 1};
+#pragma unroll
+                for (int g = 0; g < kGroups; ++g) {
+                    if (!has[g]) continue;
+                    ok = ok && __all_sync(0xFFFFFFFFu, ptx::mbar_wait(&accfull[g], phase[g], wait_ns));
+                    phase[g] ^= 1;
                 }
+                if (!ok) break;
                 ptx::tc_fence_after();
-                const uint32_t lanes = uint32_t(quad * 32) << 16, acc = tmem_base + lanes + a * N;
-                const uint32_t total = tmem_base + lanes + 2 * N;
+                const uint32_t at = tmem_base + (uint32_t(quad * 32) << 16);
 #pragma unroll
                 for (int c0 = 0; c0 < N; c0 += 16) {
-                    uint32_t v[16], t[16];
-                    ptx::tmem_ld16(acc + c0, v);
-                    if (!begins) ptx::tmem_ld16(total + c0, t);
-                    ptx::tmem_wait_ld();
-                    if (!begins) {
+                    uint32_t v[16];
+                    float sum[16] = {};
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) v[e] = __float_as_uint(__uint_as_float(t[e]) + __uint_as_float(v[e]));
+                    for (int g = 0; g < kGroups; ++g) {
+                        if (!has[g]) continue;
+                        ptx::tmem_ld16(at + g * N + c0, v);
+                        ptx::tmem_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) sum[e] += __uint_as_float(v[e]);
                     }
+                    if (!begins) {
+                        ptx::tmem_ld16(at + kGroups * N + c0, v);
+                        ptx::tmem_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) sum[e] = __uint_as_float(v[e]) + sum[e];
+                    }
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) v[e] = __float_as_uint(sum[e]);
                     if (!ends) {
-                        ptx::tmem_st16(total + c0, v);
+                        ptx::tmem_st16(at + kGroups * N + c0, v);
                     } else if (has_row) {
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
@@ -351,9 +367,11 @@ wgrad_q8_kernel(const __grid_constant__ CUtensorMap dy_map, int centre, const ui
                 }
                 if (!ends) ptx::tmem_wait_st();
                 ptx::tc_fence_before();
-                ptx::mbar_arrive(&accempty[a]);
-                ++ta;
+#pragma unroll
+                for (int g = 0; g < kGroups; ++g)
+                    if (has[g]) ptx::mbar_arrive(&accempty[g]);
             }
+            it += blocks;
         }
         if (!ok) s_abort = 1;
     } else if (warp < kMmaWarp) {
@@ -439,54 +457,53 @@ wgrad_q8_kernel(const __grid_constant__ CUtensorMap dy_map, int centre, const ui
         }
         ptx::cp_async_wait<0>();
         if (!ok) s_abort = 1;
-    } else if (warp == kMmaWarp && lane == 0) {
-        // ------------------------------------------------------------ MMA issue
-        // (This thread's instructions per block bound a map whose rows lie in L2: descriptors advance, nothing is divided.)
-        const uint64_t a_desc = ptx::desc_sw128(ptx::smem_u32(smem), 8192, 1024);
-        const uint64_t b_desc = ptx::desc_sw128(ptx::smem_u32(smem + C::kDyAt), 8192, 1024);
-        uint32_t grp = 0, tile = 0, slot = 0, tile_phase = 0;  // of the block; phase of its tile's barrier
-        uint32_t a = 0, a_phase = 1;                           // accumulator; the first waits pass
-        bool ok = true;
-        for (int i = 0; ok && i < s_work.count; ++i) {
-            int left = int((s_work.seg[i].hi - s_work.seg[i].lo + kKP - 1) / kKP);
-            uint32_t acc = 0;  // blocks in the accumulator
-            for (; left > 0; --left) {
-                if (acc == 0) {
-                    if (!ptx::mbar_wait(&accempty[a], a_phase, wait_ns)) {
+    } else if (warp < kLoadWarp) {
+        // ------------------------------------------------------------ MMA issue, a thread per group
+        if (lane == 0) {
+            const uint32_t grp = warp - kMmaWarp;
+            const uint64_t a_desc = ptx::desc_sw128(ptx::smem_u32(smem + grp * kTiles * C::kABytes), 8192, 1024);
+            const uint64_t b_desc = ptx::desc_sw128(ptx::smem_u32(smem + C::kDyAt + grp * kRing * C::kBBytes), 8192, 1024);
+            uint32_t tile = 0, slot = 0, tile_phase = 0;  // of the block; phase of its tile's barrier
+            uint32_t acc_phase = 1, it = 0;               // the first wait passes; it: the segment's first block
+            const uint32_t dcol = tmem_base + grp * N;
+            bool ok = true;
+            for (int i = 0; ok && i < s_work.count; ++i) {
+                const int blocks = int((s_work.seg[i].hi - s_work.seg[i].lo + kKP - 1) / kKP);
+                // this group's blocks of the segment
+                int left = (blocks + int((it + grp + 1) & 1)) / 2;
+                it += blocks;
+                while (ok && left > 0) {
+                    if (!ptx::mbar_wait(&accempty[grp], acc_phase, wait_ns)) {
                         ok = false;
                         break;
                     }
+                    acc_phase ^= 1;
                     ptx::tc_fence_after();
-                }
-                const uint32_t t = grp * kTiles + tile, r = grp * kRing + slot;
-                // the widened tile; its threads have seen the dy tile land
-                if (!ptx::mbar_wait(&full[t], tile_phase, wait_ns)) {
-                    ok = false;
-                    break;
-                }
-                ptx::tc_fence_after();
-                // the gathered dy rows were written by cp.async (generic proxy)
-                ptx::fence_proxy_async_smem();
-                const uint64_t ad = a_desc + t * (C::kABytes >> 4), bd = b_desc + r * (C::kBBytes >> 4);
+                    const int n = min(left, kFlush);
+                    left -= n;
+                    for (int b = 0; b < n; ++b) {
+                        // the widened tile; its threads have seen the dy tile land
+                        if (!ptx::mbar_wait(&full[grp * kTiles + tile], tile_phase, wait_ns)) {
+                            ok = false;
+                            break;
+                        }
+                        ptx::tc_fence_after();
+                        // the gathered dy rows were written by cp.async (generic proxy)
+                        ptx::fence_proxy_async_smem();
+                        const uint64_t ad = a_desc + tile * (C::kABytes >> 4), bd = b_desc + slot * (C::kBBytes >> 4);
 #pragma unroll
-                for (int ks = 0; ks < 4; ++ks)
-                    ptx::umma_f16(tmem_base + a * N, ad + ks * 128, bd + ks * 128, idesc, acc > 0 || ks > 0);
-                ptx::umma_commit(&freed[r]);
-                if (++acc == kFlush || left == 1) {
-                    ptx::umma_commit(&accfull[a]);
-                    a ^= 1;
-                    a_phase ^= a == 0;
-                    acc = 0;
-                }
-                if (++grp == kGroups) {
-                    grp = 0;
-                    slot = slot + 1 == kRing ? 0 : slot + 1;
-                    tile ^= 1;
-                    tile_phase ^= tile == 0;
+                        for (int ks = 0; ks < 4; ++ks)
+                            ptx::umma_f16(dcol, ad + ks * 128, bd + ks * 128, idesc, b > 0 || ks > 0);
+                        ptx::umma_commit(&freed[grp * kRing + slot]);
+                        slot = slot + 1 == kRing ? 0 : slot + 1;
+                        tile ^= 1;
+                        tile_phase ^= tile == 0;
+                    }
+                    if (ok) ptx::umma_commit(&accfull[grp]);
                 }
             }
+            if (!ok) s_abort = 1;
         }
-        if (!ok) s_abort = 1;
     } else if (warp == kLoadWarp && lane == 0) {
         // ------------------------------------------------------------ runs of rows
         Blocks<M / 32> blk(s_work, centre, n_in);
@@ -532,13 +549,13 @@ wgrad_q8_kernel(const __grid_constant__ CUtensorMap dy_map, int centre, const ui
     if (s_abort) {
         // A role gave up.  Before the CTA releases its TMEM and shared memory, everything still
         // writing into them must land: the gathers have (cp.async.wait_all above); the load
-        // thread waits for the run that a slot was given last, and the MMA thread commits every MMA it
-        // issued to `drain` and waits for it.  These waits have their own limit.
+        // thread waits for the run that a slot was given last, and the MMA threads commit every MMA they
+        // issued to `drain` and wait for it.  These waits have their own limit.
         bad |= (tid == 0) ? LAT_ERR_TIMEOUT : 0;
         if (warp == kLoadWarp && lane == 0)
             for (int r = 0; r < kGroups * kRing; ++r)  // (a phase whose gather warps gave up stays open: one limit for all)
                 if (s_last[r] >= 0 && !ptx::mbar_wait(&landed[r], s_last[r], kDrainNs)) break;
-        if (warp == kMmaWarp && lane == 0) {
+        if (warp >= kMmaWarp && warp < kLoadWarp && lane == 0) {
             ptx::umma_commit(drain);
             ptx::mbar_wait(drain, 0, kDrainNs);
         }
