@@ -6,7 +6,7 @@
 // shape's grid has; their number depends on the pair count and the shape alone.  A block takes
 // a share and a 64 x 64 piece of dW[k] (input channels x output channels).  For every 64 pairs
 // of a segment (the share's pairs of one offset) it widens the piece's x and dy into shared
-// memory, and each thread adds 4 x 4 products of the pairs of its group: a piece of fewer than
+// memory, and each thread adds 8 x 4 products of the pairs of its group: a piece of fewer than
 // 256 such tiles leaves threads for several groups, which take the pairs in turn and are added
 // in group order at the segment's end.  One fp32 partial per segment; wgrad_q8.cu's reduction
 // adds the partials in share order.
@@ -27,10 +27,12 @@ constexpr int kThreads = 256;
 constexpr int kBatch = 64;       // pairs in shared memory
 constexpr int kPiece = 64;       // channels of a piece, each way
 constexpr int kSharePairs = 32;  // at least
+constexpr int kTileM = 8;        // a thread's products: 8 input channels x 4 output channels
 
 __host__ __device__ inline int pieces(int c) { return (c + kPiece - 1) / kPiece; }
-// Shares at most: about four blocks per B200 SM.
-inline int most_shares(int cin, int cout) { return std::max(148, 592 / (pieces(cin) * pieces(cout))); }
+// Shares at most: the two blocks that each of a B200's 148 SMs holds (60,000 voxels, 440,000 pairs, 64 -> 64 fp32:
+// 130 us, with twice as many 137).
+inline int most_shares(int cin, int cout) { return std::max(148, 296 / (pieces(cin) * pieces(cout))); }
 
 __device__ __forceinline__ int share_count(int64_t P, int most) {
     return int(max(int64_t(P > 0), min(int64_t(most), P / kSharePairs)));
@@ -45,8 +47,9 @@ wgrad_q8_simt_kernel(const uint8_t *__restrict__ q, const uint8_t *__restrict__ 
                      int32_t *d_status) {
     pdl_enter();
     __shared__ int64_t s_off[33];
-    __shared__ int s_in[kBatch], s_out[kBatch];
-    __shared__ __align__(16) float s_x[kBatch * kPiece], s_dy[kBatch * kPiece];
+    __shared__ int s_in[2][kBatch], s_out[2][kBatch];
+    __shared__ __align__(16) float s_x[2 * kBatch * kPiece];  // x, then dy
+    float *s_dy = s_x + kBatch * kPiece;
     const int tid = threadIdx.x;
     if (tid <= k3) s_off[tid] = min(pair_off[tid], capacity);
     __syncthreads();
@@ -62,82 +65,111 @@ wgrad_q8_simt_kernel(const uint8_t *__restrict__ q, const uint8_t *__restrict__ 
     if (v >= S) return;
     const int ci0 = int(blockIdx.y) / pieces(cout) * kPiece, co0 = int(blockIdx.y) % pieces(cout) * kPiece;
     const int M = min(kPiece, cin - ci0), N = min(kPiece, cout - co0);
-    const int tiles = (M / 4) * (N / 4);
-    int lanes = 4;  // threads of a group
+    const int tiles = (M / kTileM) * (N / 4);
+    int lanes = 2;  // threads of a group
     while (lanes < tiles) lanes *= 2;
     const int groups = kThreads / lanes, group = tid / lanes, tile = tid % lanes;
     const bool has_tile = tile < tiles;
-    const int ti = has_tile ? tile / (N / 4) * 4 : 0, tj = has_tile ? tile % (N / 4) * 4 : 0;
+    const int ti = has_tile ? tile / (N / 4) * kTileM : 0, tj = has_tile ? tile % (N / 4) * 4 : 0;
     const int xg = M / 8, yg = N / 8;  // 8-channel slices of a row
     int64_t lo = P * v / S;
     const int64_t hi = P * (v + 1) / S;
     int k = 0;
     while (k < k3 && s_off[k + 1] <= lo) ++k;
     int32_t bad = 0;
+    // A batch's slices on their way: thread t has the slices t and t + kThreads of x and of dy.
+    constexpr int kMine = kBatch * kPiece / 8 / kThreads;
+    uint2 xq[kMine];
+    int xe[kMine];
+    rows::Slice8<T> yv[kMine];
+    auto pairs = [&](int64_t p0, int64_t end, int to) {  // the batch's rows, -1 for none
+        if (tid >= kBatch) return;
+        int i = -1, j = -1;
+        if (p0 + tid < end) {
+            i = __ldg(pair_in + p0 + tid);
+            j = __ldg(pair_out + p0 + tid);
+            if (i < 0 || i >= n_in || j < 0 || j >= n_out) {
+                bad |= LAT_ERR_BAD_MAP;
+                i = j = -1;
+            }
+        }
+        s_in[to][tid] = i;
+        s_out[to][tid] = j;
+    };
+    auto read = [&](int from) {
+#pragma unroll
+        for (int m = 0; m < kMine; ++m) {
+            const int o = tid + m * kThreads, px = o / xg, py = o / yg;
+            const int i = px < kBatch ? s_in[from][px] : -1, j = py < kBatch ? s_out[from][py] : -1;
+            xq[m] = make_uint2(0u, 0u);
+            xe[m] = 1;
+            if (i >= 0) rows::q8_load(q, scale, i, cin, ci0 / 8 + o % xg, xq[m], xe[m]);
+            yv[m] = j >= 0 ? rows::ld(dy + int64_t(j) * cout + co0 + o % yg * 8) : rows::zero_slice<T>();
+        }
+    };
+    auto widen = [&]() {
+#pragma unroll
+        for (int m = 0; m < kMine; ++m) {
+            const int o = tid + m * kThreads;
+            float f[8];
+            if (o < kBatch * xg) {
+                rows::q8_to_f(xq[m], xe[m], f);
+                float4 *d = reinterpret_cast<float4 *>(s_x + o * 8);
+                d[0] = make_float4(f[0], f[1], f[2], f[3]);
+                d[1] = make_float4(f[4], f[5], f[6], f[7]);
+            }
+            if (o < kBatch * yg) {
+                rows::to_f(yv[m], f);
+                float4 *d = reinterpret_cast<float4 *>(s_dy + o * 8);
+                d[0] = make_float4(f[0], f[1], f[2], f[3]);
+                d[1] = make_float4(f[4], f[5], f[6], f[7]);
+            }
+        }
+    };
     while (lo < hi) {
         const int64_t end = min(hi, s_off[k + 1]);
-        float acc[4][4] = {};
-        for (int64_t p0 = lo; p0 < end; p0 += kBatch) {
+        float2 acc[kTileM / 2][4] = {};  // two input channels each: one instruction multiplies and adds both
+        int from = 0;
+        pairs(lo, end, 0);
+        pairs(lo + kBatch, end, 1);
+        __syncthreads();
+        read(0);
+        for (int64_t p0 = lo; p0 < end; p0 += kBatch, from ^= 1) {
             const int count = int(min(int64_t(kBatch), end - p0));
-            if (tid < kBatch) {
-                int i = -1, j = -1;
-                if (tid < count) {
-                    i = __ldg(pair_in + p0 + tid);
-                    j = __ldg(pair_out + p0 + tid);
-                    if (i < 0 || i >= n_in || j < 0 || j >= n_out) {
-                        bad |= LAT_ERR_BAD_MAP;
-                        i = j = -1;
-                    }
-                }
-                s_in[tid] = i;
-                s_out[tid] = j;
-            }
+            widen();
             __syncthreads();
-            for (int o = tid; o < count * xg; o += kThreads) {
-                const int p = o / xg, c = (o % xg) * 8, i = s_in[p];
-                float f[8] = {};
-                if (i >= 0) {
-                    uint2 bits;
-                    int e;
-                    rows::q8_load(q, scale, i, cin, (ci0 + c) / 8, bits, e);
-                    rows::q8_to_f(bits, e, f);
-                }
-                float4 *d = reinterpret_cast<float4 *>(s_x + p * M + c);
-                d[0] = make_float4(f[0], f[1], f[2], f[3]);
-                d[1] = make_float4(f[4], f[5], f[6], f[7]);
+            // the next batch's rows and the pairs of the one after it, while this one is added
+            if (p0 + kBatch < end) {
+                read(from ^ 1);
+                pairs(p0 + 2 * kBatch, end, from);
             }
-            for (int o = tid; o < count * yg; o += kThreads) {
-                const int p = o / yg, c = (o % yg) * 8, j = s_out[p];
-                float f[8];
-                rows::to_f(j >= 0 ? rows::ld(dy + int64_t(j) * cout + co0 + c) : rows::zero_slice<T>(), f);
-                float4 *d = reinterpret_cast<float4 *>(s_dy + p * N + c);
-                d[0] = make_float4(f[0], f[1], f[2], f[3]);
-                d[1] = make_float4(f[4], f[5], f[6], f[7]);
-            }
-            __syncthreads();
             if (has_tile) {
 #pragma unroll 4
                 for (int p = group; p < count; p += groups) {
-                    const float4 x = *reinterpret_cast<const float4 *>(s_x + p * M + ti);
+                    const float4 x0 = *reinterpret_cast<const float4 *>(s_x + p * M + ti);
+                    const float4 x1 = *reinterpret_cast<const float4 *>(s_x + p * M + ti + 4);
                     const float4 y = *reinterpret_cast<const float4 *>(s_dy + p * N + tj);
-                    const float xv[4] = {x.x, x.y, x.z, x.w}, yv[4] = {y.x, y.y, y.z, y.w};
+                    const float2 xv[kTileM / 2] = {make_float2(x0.x, x0.y), make_float2(x0.z, x0.w),
+                                                   make_float2(x1.x, x1.y), make_float2(x1.z, x1.w)};
+                    const float2 yy[4] = {rows::both(y.x), rows::both(y.y), rows::both(y.z), rows::both(y.w)};
 #pragma unroll
-                    for (int a = 0; a < 4; ++a)
+                    for (int a = 0; a < kTileM / 2; ++a)
 #pragma unroll
-                        for (int b = 0; b < 4; ++b) acc[a][b] = fmaf(xv[a], yv[b], acc[a][b]);
+                        for (int b = 0; b < 4; ++b) acc[a][b] = rows::fma2(xv[a], yy[b], acc[a][b]);
                 }
             }
             __syncthreads();
         }
         // the groups' sums meet in shared memory: [group][M][N], in the rows' place
-        float *sums = groups > 1 ? s_x : nullptr;  // groups * M * N <= kThreads * 16 floats
+        float *sums = groups > 1 ? s_x : nullptr;  // groups * M * N <= kThreads * 32 floats
         float *out = partial + int64_t(v + k) * cin * cout + int64_t(ci0) * cout + co0;
         if (has_tile) {
 #pragma unroll
-            for (int a = 0; a < 4; ++a) {
+            for (int a = 0; a < kTileM; ++a) {
                 float4 *d = reinterpret_cast<float4 *>(sums ? sums + (group * M + ti + a) * N + tj
                                                             : out + int64_t(ti + a) * cout + tj);
-                *d = make_float4(acc[a][0], acc[a][1], acc[a][2], acc[a][3]);
+                const float2 *r = acc[a / 2];
+                *d = a & 1 ? make_float4(r[0].y, r[1].y, r[2].y, r[3].y) : make_float4(r[0].x, r[1].x, r[2].x, r[3].x);
             }
         }
         if (sums) {
