@@ -580,9 +580,12 @@ static int64_t tiles_of(int64_t n) {
 // Zeros of at least this many bytes go to the side stream: a fork and a join cost a few
 // microseconds, the zeros of 16 MB as many.
 constexpr size_t kSideBytes = size_t(16) << 20;
-// Blocks of the zeros: few, so that the sort's and the sums' reads do not queue behind their writes
-// (16,383 x 1024, 50,257 tokens: 64 us; with four times as many 71, on one stream 74).
-constexpr int kZeroBlocks = 74;
+// Blocks of the zeros beside a sort's launches: few, so that its reads and the sums' do not queue
+// behind their writes (16,383 x 1024, 50,257 tokens: 64 us; with four times as many 71, on one
+// stream 74).  Elsewhere as many as fit: behind a one-block sort the sums and the join have taken
+// every SM before the zeros' launch, and few blocks then crowd on the SMs that come free first
+// (2,048 rows x 4096, 32,000 tokens: 443 us, now 106).
+constexpr int kZeroBlocks = 74, kZeroBlocksAll = 148 * 8;
 constexpr int64_t kSmallWords = 32768;  // of the bitmap that the one-block sort clears itself
 
 // The side stream, or null where there is none to be had: creating it is left to calls outside
@@ -629,11 +632,12 @@ lat_status wgrad(const I *ids, int64_t n, const T *dy, int64_t vocab, int c, flo
     Ws w(ws, n, vocab, c);
     const int64_t words = (vocab + 31) / 32;
     const Ids<I> d{ids, vocab, pad, w.present};
+    const bool one_block = n <= kSmall && words <= kSmallWords;  // of the sort
     SideStream *side = nullptr;  // where the zeros go, if not to s
-    auto zeros = [&](cudaStream_t to) -> lat_status {
+    auto zeros = [&](cudaStream_t to, int most) -> lat_status {
         return by_lanes(c, [&](auto l) -> lat_status {
             constexpr int L = decltype(l)::value;
-            const int64_t blocks = std::min<int64_t>((vocab + kThreads / L - 1) / (kThreads / L), kZeroBlocks);
+            const int64_t blocks = std::min<int64_t>((vocab + kThreads / L - 1) / (kThreads / L), most);
             LAT_CUDA_TRY(launch_pdl(zeros_kernel<L>, dim3(unsigned(blocks)), dim3(kThreads), 0, to, w.present,
                                     uint32_t(vocab), c, dtable));
             return LAT_OK;
@@ -641,12 +645,12 @@ lat_status wgrad(const I *ids, int64_t n, const T *dy, int64_t vocab, int c, flo
     };
     auto fork_zeros = [&]() -> lat_status {  // the bitmap is complete on s
         if (size_t(vocab) * size_t(c) * sizeof(float) >= kSideBytes) side = free_side_stream(s);
-        if (!side) return zeros(s);
+        if (!side) return zeros(s, kZeroBlocksAll);
         LAT_CUDA_TRY(side_fork(*side, s));
-        return zeros(side->side);
+        return zeros(side->side, one_block ? kZeroBlocksAll : kZeroBlocks);
     };
     int at = 0;
-    if (n <= kSmall && words <= kSmallWords) {
+    if (one_block) {
         auto kern = sort_small_kernel<I>;
         LAT_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kSmallSmem)));
         LAT_CUDA_TRY(launch_pdl(kern, dim3(1), dim3(kSmallThreads), kSmallSmem, s, d, int(n), key_bits(vocab), w.key[0],
