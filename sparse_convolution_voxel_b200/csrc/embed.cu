@@ -94,19 +94,25 @@ __device__ __forceinline__ uint32_t sort_key(const Pass &p, const Ids<I> &d, int
     return uint32_t(t < 0 ? d.vocab : t);
 }
 
+constexpr int kSeenWords = 8192, kSeenTokens = 1024;  // of a block's shared memory
+static size_t seen_bytes(int64_t vocab) {
+    return 4 * size_t(vocab <= 32 * kSeenWords ? (vocab + 31) / 32 : kSeenTokens);
+}
 template <typename I, int R>
 __global__ void __launch_bounds__(kThreads) count_kernel(Pass p, Ids<I> d, int32_t *d_status) {
     pdl_enter();
     __shared__ uint32_t s_cnt[kMaxBins];
-    // Tokens of this block that are marked: a bitmap while the vocabulary fits (one word of the table's bitmap
-    // then costs a block one access; with one per distinct token 489 blocks of 1,000 tokens took 33 us, now 7),
-    // else the last token by its low bits, which keeps the frequent ones from the table's words.
-    __shared__ uint32_t s_seen[kMaxBins];
-    const bool first = !p.key_in, fits = d.vocab <= 32 * kMaxBins;
+    // Tokens of this block that are marked: a bitmap while the vocabulary fits (lanes then mark neighbouring words
+    // of the table's bitmap, each once per block: with one access per token 489 blocks of 1,000 tokens took 33 us,
+    // now 7, and 42, now 17, among 100,000 tokens), else the last token by its low bits, which keeps the frequent
+    // ones from the table's words.
+    extern __shared__ uint32_t s_seen[];
+    const bool first = !p.key_in, fits = d.vocab <= 32 * kSeenWords;
+    const int seen = fits ? int((d.vocab + 31) / 32) : kSeenTokens;
     const int bins = 1 << p.bits;
     for (int b = threadIdx.x; b < bins; b += kThreads) s_cnt[b] = 0;
     if (first)
-        for (int b = threadIdx.x; b < kMaxBins; b += kThreads) s_seen[b] = fits ? 0u : ~0u;
+        for (int b = threadIdx.x; b < seen; b += kThreads) s_seen[b] = fits ? 0u : ~0u;
     __syncthreads();
     const int64_t lo = blockIdx.x * int64_t(kThreads * R), hi = min(p.n, lo + kThreads * R);
     int32_t bad = 0;
@@ -117,15 +123,15 @@ __global__ void __launch_bounds__(kThreads) count_kernel(Pass p, Ids<I> d, int32
         if (!first || key >= d.vocab) continue;
         if (fits) {
             if (!(s_seen[key >> 5] >> (key & 31) & 1u)) atomicOr(&s_seen[key >> 5], 1u << (key & 31));
-        } else if (s_seen[key % kMaxBins] != key) {
-            s_seen[key % kMaxBins] = key;
+        } else if (s_seen[key % kSeenTokens] != key) {
+            s_seen[key % kSeenTokens] = key;
             mark(d.present, key >> 5, 1u << (key & 31));
         }
     }
     __syncthreads();
     for (int b = threadIdx.x; b < bins; b += kThreads) p.counts[int64_t(blockIdx.x) * bins + b] = s_cnt[b];
     if (first && fits)
-        for (int b = threadIdx.x; b < (d.vocab + 31) / 32; b += kThreads)
+        for (int b = threadIdx.x; b < seen; b += kThreads)
             if (s_seen[b]) mark(d.present, b, s_seen[b]);
     if (bad) flag(d_status, bad);
 }
@@ -669,7 +675,7 @@ lat_status wgrad(const I *ids, int64_t n, const T *dy, int64_t vocab, int c, flo
             const int to = i & 1;
             Pass p{i ? w.key[1 - to] : nullptr, i ? w.row[1 - to] : nullptr, w.key[to], w.row[to], w.counts, w.totals, n,
                    tiles, i * digit, digit};
-            LAT_CUDA_TRY(launch_pdl(count, dim3(tiles), dim3(kThreads), 0, s, p, d, i ? nullptr : d_status));
+            LAT_CUDA_TRY(launch_pdl(count, dim3(tiles), dim3(kThreads), i ? 0 : seen_bytes(vocab), s, p, d, i ? nullptr : d_status));
             if (i == 0) {
                 const lat_status st = fork_zeros();
                 if (st != LAT_OK) return st;
