@@ -53,9 +53,11 @@ lookup_kernel(const I *__restrict__ ids, int64_t n, const T *__restrict__ table,
     const int slices = c / 8;
     for (int vi = threadIdx.x % L + blockIdx.y * L; vi < slices; vi += L * gridDim.y) {
         float v[8] = {};
-        if (t >= 0) rows::to_f(rows::ld(table + t * c + vi * 8), v);
+        if (t >= 0) {
+            rows::to_f(rows::ld(table + t * c + vi * 8), v);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] *= scale;
+            for (int e = 0; e < 8; ++e) v[e] *= scale;
+        }
         rows::st(y + row * c + vi * 8, v);
     }
     if (bad && threadIdx.x % L == 0 && blockIdx.y == 0) flag(d_status, bad);
@@ -595,14 +597,16 @@ constexpr int kZeroBlocks = 74, kZeroBlocksAll = 148 * 8;
 constexpr int64_t kSmallWords = 32768;  // of the bitmap that the one-block sort clears itself
 
 // The side stream, or null where there is none to be had: creating it is left to calls outside
-// a capture, and one that takes part in another stream's capture is not ours to use.
+// a capture, and one that takes part in another capture is not ours to use.
 static SideStream *free_side_stream(cudaStream_t s) {
     cudaStreamCaptureStatus mine = cudaStreamCaptureStatusNone, its = cudaStreamCaptureStatusNone;
-    if (cudaStreamIsCapturing(s, &mine) != cudaSuccess) return nullptr;
+    unsigned long long my_id = 0, its_id = 0;
+    if (cudaStreamGetCaptureInfo(s, &mine, &my_id) != cudaSuccess) return nullptr;
     SideStream *side = nullptr;
     if (side_stream_slot(side) != cudaSuccess || (mine != cudaStreamCaptureStatusNone && !side->side)) return nullptr;
-    if (side_stream(side) != cudaSuccess || cudaStreamIsCapturing(side->side, &its) != cudaSuccess) return nullptr;
-    return its == cudaStreamCaptureStatusNone ? side : nullptr;
+    if (side_stream(side) != cudaSuccess || cudaStreamGetCaptureInfo(side->side, &its, &its_id) != cudaSuccess)
+        return nullptr;
+    return its == cudaStreamCaptureStatusNone || (mine == its && my_id == its_id) ? side : nullptr;
 }
 
 struct Ws {

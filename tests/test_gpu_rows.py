@@ -192,6 +192,19 @@ def test_lookup_padding_and_bad_ids():
     assert torch.allclose(out, ref, rtol=1e-6, atol=0)
 
 
+def test_rows_without_a_token_are_not_read():
+    """Padded rows come out as 0 whatever the scale is, and what their dy holds counts nowhere."""
+    table, dy = _rand(1, 20, 64), _rand(2, 5000, 64)
+    ids = _ids(3, 5000, 20, torch.int64)
+    pad = torch.arange(5000, device="cuda") % 3 == 0
+    ids[pad] = -1
+    want = scv.embed_wgrad(ids, torch.where(pad[:, None], 0.0, dy), 20)
+    dy[pad] = float("nan")
+    assert torch.equal(scv.embed_wgrad(ids, dy, 20), want)
+    for scale in (float("inf"), float("nan"), -1.0):
+        assert not scv.embed_fwd(ids, table, scale)[pad].view(torch.int32).any()
+
+
 def test_lookup_gradient_without_a_token():
     dy = _rand(4, 5000, 128)
     ids = torch.full((5000,), -1, dtype=torch.int32, device="cuda")
@@ -557,6 +570,23 @@ def test_lookup_gradient_of_a_large_table_captured():
     thread.start()
     thread.join()
     assert len(got) == 4 and all(torch.equal(o, want) for o in got)
+
+
+def test_lookup_gradients_in_one_capture():
+    """Two of them in a row share the side stream and the workspace."""
+    ids = [_ids(i, n, 40000, torch.int64) for i, n in enumerate((9000, 300))]
+    dy = [_rand(i, n, 128) for i, n in enumerate((9000, 300))]
+    want = [scv.embed_wgrad(i, d, 40000) for i, d in zip(ids, dy)]
+    ws = scv.Workspace()
+    out = [scv.embed_wgrad(i, d, 40000, ws=ws).fill_(float("nan")) for i, d in zip(ids, dy)]
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        for i, d, o in zip(ids, dy, out):
+            scv.embed_wgrad(i, d, 40000, ws=ws, out=o)
+    for _ in range(3):
+        g.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, w) for o, w in zip(out, want))
 
 
 def test_two_streams_at_once():
