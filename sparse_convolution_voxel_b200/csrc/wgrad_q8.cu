@@ -97,7 +97,13 @@ struct Work {
     Segment seg[kMaxSegments];
     __device__ void make(const int64_t *pair_off, int64_t capacity, int k3, int worker, int32_t *ranges) {
         const int lane = threadIdx.x & 31;
-        for (int e = lane; e <= k3; e += 32) off[e] = min(pair_off[e], capacity);
+        // whatever the offsets hold, they rise from 0 here to at most the capacity, which bounds the segments and slots
+        auto read = [&](int e) { return e <= k3 ? max(int64_t(0), min(pair_off[e], capacity)) : int64_t(0); };
+        int64_t upper = read(lane);
+#pragma unroll
+        for (int m = 1; m < 32; m <<= 1) upper = max(upper, int64_t(__shfl_up_sync(0xFFFFFFFFu, (long long)upper, m)));
+        off[lane] = upper;
+        if (lane == 31) off[32] = max(upper, read(32));
         __syncwarp();
         const int64_t P = off[k3];
         const int S = int(max(int64_t(P > 0), min(int64_t(kWorkers * kTurns), P / kKP)));
