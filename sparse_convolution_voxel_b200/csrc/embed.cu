@@ -19,11 +19,12 @@
 // other rows too.  Where these are many megabytes, a kernel of its own does, on a side stream,
 // while the sort and the sums, which wait for latencies more than for bandwidth, go on.
 //
-// A chain of four launches up to 4,096 rows, seven or ten beyond: each takes 2 us and more, the
+// A chain of three launches up to 4,096 rows, six or nine beyond: each takes 2 us and more, the
 // sums of 500k x 128 rows 30 us of the call's 60 (4.2 TB/s of random rows).
 #include <algorithm>
 
 #include "rows.cuh"
+#include "tc_ptx.cuh"
 
 namespace lat {
 namespace embed {
@@ -491,68 +492,127 @@ __global__ void __launch_bounds__(kThreads, 3) sums_kernel(Runs p, const T *__re
 
 // Tokens whose run crosses a cut: for each listed share v the run is tail[v], then the heads
 // of the shares up to the one that holds the run's end, where a sums block that lies between
-// v's and the last one's has one head for all its shares.  Row t of kJoinRows adds the parts
-// t, t + kJoinRows, ... in order, then the rows' sums are added in order.  The list's order
-// does not matter: every token is the sum of one entry.  (Stores the zeros too, see Runs::present:
-// 2 us less than by a launch of their own.)
-constexpr int kJoinRows = 8, kJoinBlocks = 1184;
+// v's and the last one's has one head for all its shares.  A block takes a run: row t of
+// kJoinRows adds the parts t, t + kJoinRows, ... in order, then the rows' sums are added in
+// order.  Where there are more runs than blocks, a warp takes a run of up to kShort parts by
+// itself and adds them in order (7,000 runs of 500k x 128 rows of 100,000 tokens: 10.5 us, with
+// a block for each 16).  The list's order does not matter: every token is the sum of one entry.
+// Stores the zeros too, see Runs::present: 2 us less than by a launch of their own.
+constexpr int kJoinRows = 8, kJoinBlocks = 1184, kShort = 16;
 __global__ void __launch_bounds__(32 * kJoinRows) join_kernel(Runs p, int per_block) {
     pdl_enter();
     __shared__ float4 s[kJoinRows][32];
+    __shared__ int s_long[kJoinRows];
     const int count = *p.open_count, col = (blockIdx.y * 32 + threadIdx.x) * 4;
-    if (p.present && col < p.c)
+    const bool own = col < p.c;
+    if (p.present && own)
         for (uint32_t r = blockIdx.x * kJoinRows + threadIdx.y; r < p.vocab; r += gridDim.x * kJoinRows)
             if (!((__ldg(p.present + (r >> 5)) >> (r & 31)) & 1u))
                 *reinterpret_cast<float4 *>(p.dtable + int64_t(r) * p.c + col) = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int o = blockIdx.x; o < count; o += gridDim.x) {
-        const int2 run = p.open[o];
-        const int v = run.x;
-        const uint32_t token = uint32_t(run.y);
-        const int last = p.last[token];
+    struct Run {
+        int v, token, last, lead, blocks, parts;
+    };
+    auto run_of = [&](int o) {
+        const int2 open = p.open[o];
+        Run r{open.x, open.y, p.last[open.y], 0, 0, 0};
         // shares v .. end of v's block, whole blocks, then the shares of the last block
-        const int block = v / per_block, blocks = max(0, last / per_block - block - 1);
-        const int lead = min(last, (block + 1) * per_block - 1) - v + 1;
-        const int parts = blocks > 0 ? lead + blocks + last % per_block + 1 : last - v + 1;
+        const int block = r.v / per_block;
+        r.blocks = max(0, r.last / per_block - block - 1);
+        r.lead = min(r.last, (block + 1) * per_block - 1) - r.v + 1;
+        r.parts = r.blocks > 0 ? r.lead + r.blocks + r.last % per_block + 1 : r.last - r.v + 1;
+        return r;
+    };
+    auto part = [&](const Run &r, int q) {
+        int64_t at = r.v + q;
+        if (r.blocks > 0 && q >= r.lead)
+            at = q < r.lead + r.blocks ? (r.v / per_block + 1 + q - r.lead) * per_block : r.last - (r.parts - 1 - q);
+        return *reinterpret_cast<const float4 *>((q == 0 ? p.tail : p.head) + at * p.c + col);
+    };
+    auto add = [](float4 &a, const float4 &x) {
+        a.x += x.x;
+        a.y += x.y;
+        a.z += x.z;
+        a.w += x.w;
+    };
+    auto store = [&](const Run &r, const float4 &a) {
+        *reinterpret_cast<float4 *>(p.dtable + int64_t(r.token) * p.c + col) =
+            make_float4(a.x * p.scale, a.y * p.scale, a.z * p.scale, a.w * p.scale);
+    };
+    auto by_block = [&](int o) {
+        const Run r = run_of(o);
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        auto add = [&](const float4 &x) {
-            acc.x += x.x;
-            acc.y += x.y;
-            acc.z += x.z;
-            acc.w += x.w;
-        };
-        if (col < p.c) {
+        if (own) {
 #pragma unroll 4
-            for (int q = threadIdx.y; q < parts; q += kJoinRows) {
-                int64_t at = v + q;
-                if (blocks > 0 && q >= lead)
-                    at = q < lead + blocks ? (block + 1 + q - lead) * per_block : last - (parts - 1 - q);
-                add(*reinterpret_cast<const float4 *>((q == 0 ? p.tail : p.head) + at * p.c + col));
-            }
+            for (int q = threadIdx.y; q < r.parts; q += kJoinRows) add(acc, part(r, q));
         }
         s[threadIdx.y][threadIdx.x] = acc;
         __syncthreads();
-        if (threadIdx.y == 0 && col < p.c) {
+        if (threadIdx.y == 0 && own) {
 #pragma unroll
-            for (int q = 1; q < kJoinRows; ++q) add(s[q][threadIdx.x]);
-            *reinterpret_cast<float4 *>(p.dtable + int64_t(token) * p.c + col) =
-                make_float4(acc.x * p.scale, acc.y * p.scale, acc.z * p.scale, acc.w * p.scale);
+            for (int q = 1; q < kJoinRows; ++q) add(acc, s[q][threadIdx.x]);
+            store(r, acc);
         }
+    };
+    if (count <= int(gridDim.x)) {
+        if (int(blockIdx.x) < count) by_block(blockIdx.x);
+        return;
+    }
+    for (int o0 = blockIdx.x; o0 < count; o0 += gridDim.x * kJoinRows) {
+        const int o = o0 + int(gridDim.x * threadIdx.y);
+        bool long_run = false;
+        if (o < count) {
+            const Run r = run_of(o);
+            long_run = r.parts > kShort;
+            if (own && !long_run) {
+                float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+                for (int q = 0; q < r.parts; ++q) add(acc, part(r, q));
+                store(r, acc);
+            }
+        }
+        if (!__syncthreads_or(long_run)) continue;
+        if (threadIdx.x == 0) s_long[threadIdx.y] = long_run ? o : -1;
         __syncthreads();
+        for (int w = 0; w < kJoinRows; ++w) {
+            if (s_long[w] < 0) continue;
+            by_block(s_long[w]);
+            __syncthreads();
+        }
     }
 }
 
-// Zeros for the tokens without rows, where the join does not store them: L lanes take a table row.
-template <int L>
-__global__ void __launch_bounds__(kThreads)
-zeros_kernel(const uint32_t *__restrict__ present, uint32_t vocab, int c, float *__restrict__ dtable) {
+// Zeros for the tokens without rows, where the join does not store them.  A warp takes `tokens`
+// of them at a time (a power of two up to 32): each run of absent ones is a piece of the table
+// without a gap, written by bulk stores from a buffer of zeros.  (Stores from registers fill the
+// load and store units: 117 us for 32,768 rows x 512, 131,072 tokens, now 72.)
+constexpr int kZeroThreads = 128, kZeroWarps = kZeroThreads / 32;
+constexpr uint32_t kZeroBytes = 16384;  // of the buffer
+__global__ void __launch_bounds__(kZeroThreads)
+zeros_kernel(const uint32_t *__restrict__ present, uint32_t vocab, uint32_t tokens, uint32_t row_bytes,
+             uint8_t *__restrict__ dtable) {
     pdl_enter();
-    const float zero[8] = {};
-    const uint32_t stride = gridDim.x * (kThreads / L);
-    for (uint64_t r = blockIdx.x * (kThreads / L) + threadIdx.x / L; r < vocab; r += stride) {
-        if ((__ldg(present + (r >> 5)) >> (r & 31)) & 1u) continue;
-        float *at = dtable + int64_t(r) * c;
-        for (int vi = threadIdx.x % L; vi < c / 8; vi += L) rows::st(at + vi * 8, zero);
+    __shared__ uint4 s_zero[kZeroBytes / 16];
+    for (int i = threadIdx.x; i < int(kZeroBytes / 16); i += kZeroThreads) s_zero[i] = make_uint4(0u, 0u, 0u, 0u);
+    ptx::fence_proxy_async_smem();
+    __syncthreads();
+    const uint32_t lane = threadIdx.x & 31, stride = gridDim.x * kZeroWarps * tokens;
+    for (uint64_t t = (blockIdx.x * kZeroWarps + (threadIdx.x >> 5)) * tokens; t < vocab; t += stride) {
+        uint32_t absent = ~__ldg(present + (t >> 5)) >> (t & 31);
+        const uint32_t here = uint32_t(min(uint64_t(tokens), vocab - t));
+        if (here < 32) absent &= (1u << here) - 1u;
+        const uint32_t from = absent >> lane;  // this lane's token and those behind it
+        if (!(from & 1u) || (lane > 0 && ((absent >> (lane - 1)) & 1u))) continue;  // no run begins here
+        const uint32_t count = from == ~0u ? 32u : uint32_t(__ffs(int(~from))) - 1u;
+        uint8_t *at = dtable + (t + lane) * row_bytes;
+        for (uint32_t left = count * row_bytes; left > 0;) {
+            const uint32_t bytes = min(left, kZeroBytes);
+            ptx::bulk_store(at, s_zero, bytes);
+            at += bytes;
+            left -= bytes;
+        }
     }
+    ptx::bulk_store_commit();
+    ptx::bulk_store_wait();
 }
 
 // ----------------------------------------------------------------------------- host
@@ -593,15 +653,13 @@ static int64_t tiles_of(int64_t n) {
     return std::max<int64_t>(1, (n + tile - 1) / tile);
 }
 
-// Zeros of at least this many bytes go to the side stream: a fork and a join cost a few
-// microseconds, the zeros of 16 MB as many.
-constexpr size_t kSideBytes = size_t(16) << 20;
-// Blocks of the zeros beside a sort's launches: few, so that its reads and the sums' do not queue
-// behind their writes (16,383 x 1024, 50,257 tokens: 64 us; with four times as many 71, on one
-// stream 74).  Elsewhere as many as fit: behind a one-block sort the sums and the join have taken
-// every SM before the zeros' launch, and few blocks then crowd on the SMs that come free first
-// (2,048 rows x 4096, 32,000 tokens: 443 us, now 106).
-constexpr int kZeroBlocks = 74, kZeroBlocksAll = 148 * 8;
+// Zeros of at least this many bytes have a kernel of their own: with the launches of a sort ahead
+// on the side stream (a fork and a join cost a few microseconds, the zeros of 16 MB as many);
+// behind a one-block sort in front of the sums, which are short.  (Beside those it came after the
+// sums' and the join's blocks had taken every SM, and crowded on the first that came free: 443 us
+// for 2,048 rows x 4096, 32,000 tokens, now 107.)
+constexpr size_t kLargeBytes = size_t(16) << 20;
+constexpr int kZeroBlocks = 592;  // 32,768 rows x 512, 131,072 tokens: 85 us with 74 blocks, 80 with 148, 75 with 296, 72 with 592 and more
 constexpr int64_t kSmallWords = 32768;  // of the bitmap that the one-block sort clears itself
 
 // The side stream, or null where there is none to be had: creating it is left to calls outside
@@ -651,30 +709,26 @@ lat_status wgrad(const I *ids, int64_t n, const T *dy, int64_t vocab, int c, flo
     const int64_t words = (vocab + 31) / 32;
     const Ids<I> d{ids, vocab, pad, w.present};
     const bool one_block = n <= kSmall && words <= kSmallWords;  // of the sort
-    SideStream *side = nullptr;  // where the zeros go, if not to s
-    auto zeros = [&](cudaStream_t to, int most) -> lat_status {
-        return by_lanes(c, [&](auto l) -> lat_status {
-            constexpr int L = decltype(l)::value;
-            const int64_t blocks = std::min<int64_t>((vocab + kThreads / L - 1) / (kThreads / L), most);
-            LAT_CUDA_TRY(launch_pdl(zeros_kernel<L>, dim3(unsigned(blocks)), dim3(kThreads), 0, to, w.present,
-                                    uint32_t(vocab), c, dtable));
-            return LAT_OK;
-        });
+    SideStream *side = nullptr;  // where the zeros of a large table go
+    auto zeros = [&](cudaStream_t to) -> lat_status {
+        uint32_t tokens = 32;  // of a warp at a time: some 64 KB of zeros
+        while (tokens > 1 && tokens * uint32_t(c) * 4 > 65536) tokens /= 2;
+        const int64_t blocks = std::min<int64_t>((vocab + tokens * kZeroWarps - 1) / (tokens * kZeroWarps), kZeroBlocks);
+        LAT_CUDA_TRY(launch_pdl(zeros_kernel, dim3(unsigned(blocks)), dim3(kZeroThreads), 0, to, w.present,
+                                uint32_t(vocab), tokens, uint32_t(c) * 4, reinterpret_cast<uint8_t *>(dtable)));
+        return LAT_OK;
     };
-    auto fork_zeros = [&]() -> lat_status {  // the bitmap is complete on s
-        if (size_t(vocab) * size_t(c) * sizeof(float) >= kSideBytes) side = free_side_stream(s);
-        if (!side) return n > 0 ? LAT_OK : zeros(s, kZeroBlocksAll);  // else the join's
-        LAT_CUDA_TRY(side_fork(*side, s));
-        return zeros(side->side, one_block ? kZeroBlocksAll : kZeroBlocks);
-    };
+    const bool joined = n > 0 && size_t(vocab) * size_t(c) * sizeof(float) < kLargeBytes;  // the zeros are the join's
     int at = 0;
     if (one_block) {
         auto kern = sort_small_kernel<I>;
         LAT_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kSmallSmem)));
         LAT_CUDA_TRY(launch_pdl(kern, dim3(1), dim3(kSmallThreads), kSmallSmem, s, d, int(n), key_bits(vocab), w.key[0],
                                 w.row[0], w.open_count, d_status));
-        const lat_status st = fork_zeros();
-        if (st != LAT_OK) return st;
+        if (!joined) {
+            const lat_status st = zeros(s);
+            if (st != LAT_OK) return st;
+        }
     } else {
         LAT_CUDA_TRY(fill_u32(w.present, words, 0u, s));
         const int bits = key_bits(vocab), passes = (bits + kMaxBits - 1) / kMaxBits;
@@ -688,8 +742,9 @@ lat_status wgrad(const I *ids, int64_t n, const T *dy, int64_t vocab, int c, flo
             Pass p{i ? w.key[1 - to] : nullptr, i ? w.row[1 - to] : nullptr, w.key[to], w.row[to], w.counts, w.totals, n,
                    tiles, i * digit, digit};
             LAT_CUDA_TRY(launch_pdl(count, dim3(tiles), dim3(kThreads), i ? 0 : seen_bytes(vocab), s, p, d, i ? nullptr : d_status));
-            if (i == 0) {
-                const lat_status st = fork_zeros();
+            if (i == 0 && !joined) {  // the bitmap is complete on s
+                if ((side = free_side_stream(s)) != nullptr) LAT_CUDA_TRY(side_fork(*side, s));
+                const lat_status st = zeros(side ? side->side : s);
                 if (st != LAT_OK) return st;
             }
             LAT_CUDA_TRY(launch_pdl(tile_scan_kernel, dim3((bins + kScanBins - 1) / kScanBins), dim3(kScanBins, kScanRows), 0, s, w.counts, w.totals,
@@ -700,7 +755,7 @@ lat_status wgrad(const I *ids, int64_t n, const T *dy, int64_t vocab, int c, flo
     }
     if (n > 0) {
         Runs p{w.key[at], w.row[at], uint32_t(n), uint32_t(vocab), 0, run_shares(n, c), c, scale, w.head, w.tail, w.open,
-               w.open_count, w.last, dtable, side ? nullptr : w.present};
+               w.open_count, w.last, dtable, joined ? w.present : nullptr};
         p.share = uint32_t((n + p.shares - 1) / p.shares);
         const int groups = kThreads / lanes_of(c), slabs = (c / 8 + 31) / 32, beside = std::min(slabs, groups);
         const int per_block = groups / beside;
@@ -713,7 +768,7 @@ lat_status wgrad(const I *ids, int64_t n, const T *dy, int64_t vocab, int c, flo
         });
         if (st != LAT_OK) return st;
         const int cols = (c + 127) / 128, most = std::max(1, kJoinBlocks / cols);
-        LAT_CUDA_TRY(launch_pdl(join_kernel, dim3(unsigned(side ? std::min(p.shares, most) : most), unsigned(cols)),
+        LAT_CUDA_TRY(launch_pdl(join_kernel, dim3(unsigned(joined ? most : std::min(p.shares, most)), unsigned(cols)),
                                 dim3(32, kJoinRows), 0, s, p, per_block));
     }
     if (side) LAT_CUDA_TRY(side_join(*side, s));

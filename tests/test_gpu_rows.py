@@ -148,6 +148,7 @@ def test_lookup(dtype, idt, n, vocab, c):
     (5000, 700, 128), (5000, 100000, 8), (20000, 1 << 10, 64), (20000, 3000000, 8), (4096, 64, 512),
     (3000, 17, 1032), (70000, 300, 32), (150000, 5, 128), (4096, 255, 8), (4097, 256, 8), (8191, 70000, 16),
     (65536, 300, 8), (65537, 40000, 8), (33000, 1, 16), (5000, 1100000, 8), (4100, 262144, 8), (4100, 262145, 8),
+    (0, 40000, 128), (0, 1100000, 8), (100, 700, 8192), (5000, 700, 8192), (4097, 260, 16384), (300000, 50000, 64),
 ])
 @pytest.mark.parametrize("dtype,idt", [(torch.float32, torch.int32), (torch.bfloat16, torch.int64)])
 def test_lookup_gradient(n, vocab, c, dtype, idt):
