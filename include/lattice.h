@@ -394,15 +394,19 @@ lat_status lat_to_dense(const int32_t *coords, int64_t n, const void *feats, int
  *           0 and its dy counts nowhere.  Another id outside [0, vocab) does
  *           the same and sets LAT_ERR_BAD_ID at d_status (may be NULL).
  *   table   device [vocab][c], y and dy device [n][c], of dtype, aligned to
- *           8 channels (16 bytes, fp32 32), without overlap; c a multiple of 8 in [8, 16384];
- *           n < 2^31, 1 <= vocab < 2^31 - 1.
+ *           8 channels (16 bytes, fp32 32), without overlap; c a multiple of
+ *           8 in [8, 16384]; n < 2^31, 1 <= vocab < 2^31 - 1.
  *   dtable  device fp32 [vocab][c], 32-byte aligned; every row is written
  *           (0 for a token without rows).
  * Arithmetic is fp32, one rounding to dtype.  The gradient sorts the rows by
  * token and adds each token's rows in parts whose sizes and order depend on
  * the arguments' sizes alone (no atomics on sums): its bits are the same on
  * every call.  Workspace as for the other ops (32-byte aligned); lookup
- * takes none.  Asynchronous on `stream`; allocates nothing. */
+ * takes none.  Asynchronous on `stream`; allocates no memory.  A gradient of
+ * 16 MB and more writes its zeros on a stream of the calling thread's own,
+ * between an event that `stream` records and one that it waits for; the
+ * thread's first such call outside a capture creates it, and a capture
+ * before that goes without. */
 lat_status lat_embed_fwd(const void *ids, int32_t id_bytes, int64_t n, const void *table, int64_t vocab,
                          int32_t c, float scale, int64_t pad_id, void *y, lat_dtype dtype,
                          int32_t *d_status, lat_stream stream);
@@ -438,7 +442,9 @@ lat_status lat_q8_unpack(const void *q, const void *scale, int64_t n, int32_t c,
  * (i, j) of offset k of (q * scale)[i]^T dy[j], fp32.  dtype is dy's (16-byte
  * aligned, fp32 32); scale 4-byte aligned.  Limits and errors as for
  * lat_sconv_wgrad.  Deterministic in the same way; the number of shares
- * depends on the pair count and the channel counts alone. */
+ * depends on the pair count and the channel counts alone.  In a map of mode
+ * LAT_SUBM pair m of the centre offset is (m, m), as lat_kmap_query writes
+ * it: those rows are copied by their number, not by the pair list. */
 size_t lat_sconv_wgrad_q8_ws_bytes(int32_t cin, int32_t cout, const lat_kmap *map, lat_dtype dtype);
 lat_status lat_sconv_wgrad_q8(const void *q, const void *scale, int32_t cin, const void *dy, int32_t cout,
                               const lat_kmap *map, float *dw, lat_dtype dtype, void *ws, size_t ws_bytes,
@@ -466,9 +472,9 @@ lat_status lat_rms_norm_fwd(const void *x, const void *res, const void *w, int64
  * dh: the gradient that reaches h past the norm, NULL for none.  dx may be
  * dy or dh itself; no other overlap.  The sums of dw run in a fixed order
  * over parts that depend on n and c alone.  Workspace (32-byte aligned) only
- * for dw.  Both passes: rows and w aligned to 8 channels (16 bytes, fp32
- * 32), 8-bit values to 16 bytes, c a multiple of 8 in [8, 16384], n < 2^31, fp32 arithmetic; asynchronous on `stream`; they
- * allocate nothing. */
+ * for dw.  Both passes: rows and w aligned to 8 channels (16 bytes, fp32 32),
+ * 8-bit values to 16 bytes, c a multiple of 8 in [8, 16384], n < 2^31, fp32
+ * arithmetic; asynchronous on `stream`; they allocate nothing. */
 size_t lat_rms_norm_bwd_ws_bytes(int64_t n, int32_t c);
 lat_status lat_rms_norm_bwd(const void *dy, const void *dh, const void *h, const void *h8,
                             const void *h8_scale, const float *rstd, const void *w, int64_t n, int32_t c,

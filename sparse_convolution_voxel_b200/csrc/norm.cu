@@ -17,7 +17,8 @@
 // with cp.async into a ring of its own in shared memory -- it alone reads them, so its own
 // copies are all it waits for -- which keeps some 150 KB per SM in flight without the
 // registers that loads ahead would take (500k x 128 bf16 from 8-bit rows, 450 MB: 98 us with
-// a row's loads in front of its work, 106 us with the next row in registers, 89 us so).
+// a row's loads in front of its work, 106 us with the next row in registers, 89 us so; 81 with
+// offsets that advance and two fp32 operations per instruction, of which 6 are dw's second kernel).
 //
 // dw: a fixed number of blocks (never more than there are row groups) walks the rows in
 // fixed steps with the sums of its rows in registers, adds its groups' sums in order in
