@@ -80,7 +80,8 @@ struct Pass {
     const uint32_t *key_in, *row_in;  // null: the ids themselves (first pass)
     uint32_t *key_out, *row_out;
     uint32_t *counts;   // [tiles][bins]: rows of the tile with the digit, then (scan) those of earlier tiles
-    uint32_t *totals;   // [bins]
+    uint32_t *totals;   // [bins]; null: the counts are not scanned, the scatter's blocks do it
+    int32_t *open_count;  // of the sums' list, cleared by the count
     int64_t n;
     int tiles, shift, bits;
 };
@@ -117,6 +118,7 @@ __global__ void __launch_bounds__(kThreads) count_kernel(Pass p, Ids<I> d, int32
     const int seen = fits ? int((d.vocab + 31) / 32) : kSeenTokens;
     const int bins = 1 << p.bits;
     for (int b = threadIdx.x; b < bins; b += kThreads) s_cnt[b] = 0;
+    if (blockIdx.x == 0 && threadIdx.x == 0) *p.open_count = 0;
     if (first)
         for (int b = threadIdx.x; b < seen; b += kThreads) s_seen[b] = fits ? 0u : ~0u;
     __syncthreads();
@@ -143,13 +145,10 @@ __global__ void __launch_bounds__(kThreads) count_kernel(Pass p, Ids<I> d, int32
 }
 
 // 8 digit values per block, 128 threads each: thread row t takes a run of the tiles.
-// (Also clears the count of open runs for the sums.)
 constexpr int kScanBins = 8, kScanRows = 128;
 __global__ void __launch_bounds__(kScanBins * kScanRows)
-tile_scan_kernel(uint32_t *__restrict__ counts, uint32_t *__restrict__ totals, int tiles, int bins,
-                 int32_t *__restrict__ open_count) {
+tile_scan_kernel(uint32_t *__restrict__ counts, uint32_t *__restrict__ totals, int tiles, int bins) {
     pdl_enter();
-    if (blockIdx.x == 0 && threadIdx.x == 0 && threadIdx.y == 0) *open_count = 0;
     __shared__ uint32_t s[2][kScanRows][kScanBins];
     const int b = blockIdx.x * kScanBins + threadIdx.x, t = threadIdx.y;
     const int per = (tiles + kScanRows - 1) / kScanRows, lo = min(tiles, t * per), hi = min(tiles, lo + per);
@@ -223,9 +222,32 @@ __global__ void __launch_bounds__(kThreads) scatter_kernel(Pass p, Ids<I> d) {
     }
     const bool own = int(threadIdx.x) * 4 < bins;  // this thread's digits 4 t .. 4 t + 3
     uint4 total = make_uint4(0u, 0u, 0u, 0u), start = total;
-    if (own) {
+    auto add4 = [](uint4 &a, const uint4 &v) { a = make_uint4(a.x + v.x, a.y + v.y, a.z + v.z, a.w + v.w); };
+    if (!p.totals) {
+        // thread row g of four digits per thread adds the tiles g, g + rows, ...; then the rows meet
+        const int quads = bins / 4, tile_rows = kThreads / quads, g = threadIdx.x / quads;
+#pragma unroll 8
+        for (int t = g; t < p.tiles; t += tile_rows) {
+            const uint4 v = reinterpret_cast<const uint4 *>(p.counts + int64_t(t) * bins)[threadIdx.x % quads];
+            add4(total, v);
+            if (t < int(blockIdx.x)) add4(start, v);
+        }
+        s_cnt4[0][threadIdx.x] = total;
+        s_cnt4[1][threadIdx.x] = start;
+        __syncthreads();
+        if (own)
+            for (int o = 1; o < min(tile_rows, p.tiles); ++o) {
+                add4(total, s_cnt4[0][o * quads + threadIdx.x]);
+                add4(start, s_cnt4[1][o * quads + threadIdx.x]);
+            }
+        else
+            total = make_uint4(0u, 0u, 0u, 0u);
+        __syncthreads();
+    } else if (own) {
         total = reinterpret_cast<const uint4 *>(p.totals)[threadIdx.x];
         start = reinterpret_cast<const uint4 *>(p.counts + int64_t(blockIdx.x) * bins)[threadIdx.x];
+    }
+    if (own) {
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) s_cnt4[w][threadIdx.x] = make_uint4(0u, 0u, 0u, 0u);
     }
@@ -653,6 +675,11 @@ static int64_t tiles_of(int64_t n) {
     return std::max<int64_t>(1, (n + tile - 1) / tile);
 }
 
+// Up to this many counts (tiles x digit values) every block of the scatter scans them itself, a
+// launch less in every pass: 32 tiles x 256 digit values 1 us less in a call of 64, 64 x 256 the
+// same either way, 32 x 1024 3 us more.
+constexpr int64_t kFewCounts = 8192;
+
 // Zeros of at least this many bytes have a kernel of their own: with the launches of a sort ahead
 // on the side stream (a fork and a join cost a few microseconds, the zeros of 16 MB as many);
 // behind a one-block sort in front of the sums, which are short.  (Beside those it came after the
@@ -734,21 +761,22 @@ lat_status wgrad(const I *ids, int64_t n, const T *dy, int64_t vocab, int c, flo
         const int bits = key_bits(vocab), passes = (bits + kMaxBits - 1) / kMaxBits;
         const int digit = std::max(2, (bits + passes - 1) / passes), tiles = int(tiles_of(n));
         const int bins = 1 << digit;
-        const bool few = tile_rounds(n) == 2;
+        const bool few = tile_rounds(n) == 2, scan = int64_t(tiles) * bins > kFewCounts;
         auto count = few ? count_kernel<I, 2> : count_kernel<I, 4>;
         auto scatter = few ? scatter_kernel<I, 2> : scatter_kernel<I, 4>;
         for (int i = 0; i < passes; ++i) {
             const int to = i & 1;
-            Pass p{i ? w.key[1 - to] : nullptr, i ? w.row[1 - to] : nullptr, w.key[to], w.row[to], w.counts, w.totals, n,
-                   tiles, i * digit, digit};
+            Pass p{i ? w.key[1 - to] : nullptr, i ? w.row[1 - to] : nullptr, w.key[to], w.row[to], w.counts,
+                   scan ? w.totals : nullptr, w.open_count, n, tiles, i * digit, digit};
             LAT_CUDA_TRY(launch_pdl(count, dim3(tiles), dim3(kThreads), i ? 0 : seen_bytes(vocab), s, p, d, i ? nullptr : d_status));
             if (i == 0 && !joined) {  // the bitmap is complete on s
                 if ((side = free_side_stream(s)) != nullptr) LAT_CUDA_TRY(side_fork(*side, s));
                 const lat_status st = zeros(side ? side->side : s);
                 if (st != LAT_OK) return st;
             }
-            LAT_CUDA_TRY(launch_pdl(tile_scan_kernel, dim3((bins + kScanBins - 1) / kScanBins), dim3(kScanBins, kScanRows), 0, s, w.counts, w.totals,
-                                    tiles, bins, w.open_count));
+            if (scan)
+                LAT_CUDA_TRY(launch_pdl(tile_scan_kernel, dim3((bins + kScanBins - 1) / kScanBins),
+                                        dim3(kScanBins, kScanRows), 0, s, w.counts, w.totals, tiles, bins));
             LAT_CUDA_TRY(launch_pdl(scatter, dim3(tiles), dim3(kThreads), 0, s, p, d));
             at = to;
         }
