@@ -19,8 +19,8 @@
 // other rows too.  Where these are many megabytes, a kernel of its own does, on a side stream,
 // while the sort and the sums, which wait for latencies more than for bandwidth, go on.
 //
-// A chain of three launches up to 4,096 rows, six or nine beyond: each takes 2 us and more, the
-// sums of 500k x 128 rows 30 us of the call's 60 (4.2 TB/s of random rows).
+// A chain of three launches up to 4,096 rows, five to nine beyond: each takes 2 us and more, the
+// sums of 500k x 128 rows 30 us of the call's 55 (4.2 TB/s of random rows).
 #include <algorithm>
 
 #include "rows.cuh"
@@ -226,7 +226,7 @@ __global__ void __launch_bounds__(kThreads) scatter_kernel(Pass p, Ids<I> d) {
     if (!p.totals) {
         // thread row g of four digits per thread adds the tiles g, g + rows, ...; then the rows meet
         const int quads = bins / 4, tile_rows = kThreads / quads, g = threadIdx.x / quads;
-#pragma unroll 8
+#pragma unroll 16
         for (int t = g; t < p.tiles; t += tile_rows) {
             const uint4 v = reinterpret_cast<const uint4 *>(p.counts + int64_t(t) * bins)[threadIdx.x % quads];
             add4(total, v);
@@ -676,9 +676,10 @@ static int64_t tiles_of(int64_t n) {
 }
 
 // Up to this many counts (tiles x digit values) every block of the scatter scans them itself, a
-// launch less in every pass: 32 tiles x 256 digit values 1 us less in a call of 64, 64 x 256 the
-// same either way, 32 x 1024 3 us more.
-constexpr int64_t kFewCounts = 8192;
+// launch less in every pass.  These calls wait for their launches: 8,192 rows of 1,000 tokens
+// 25 us, with the scan 28; 24,000 of 50,000 tokens 32, with it 38.  (On the GPU alone 32 tiles x
+// 1024 digit values take 2 us more so, 128 x 512 take 20.)
+constexpr int64_t kFewCounts = 32768;
 
 // Zeros of at least this many bytes have a kernel of their own: with the launches of a sort ahead
 // on the side stream (a fork and a join cost a few microseconds, the zeros of 16 MB as many);
