@@ -81,7 +81,8 @@ def check_status(d_status: torch.Tensor, where: str = "device status"):
 
 
 class Workspace:
-    """Grow-only device scratch buffer handed to the *_ws arguments."""
+    """Grow-only device scratch buffer handed to the *_ws arguments.  A captured graph holds the
+    buffer's address: let it grow to the largest call before a capture."""
 
     def __init__(self, device="cuda"):
         self.device = torch.device(device)
@@ -301,8 +302,9 @@ def _vector_like(x, n: int):
 
 def embed_fwd(ids, table, scale: float = 1.0, pad_id: int = -1, d_status=None, out=None, stream=None):
     """scale * table[ids] (n, c); rows whose id is pad_id are 0.  ids int32 or int64 (n,)."""
+    (n,), (_, c) = ids.shape, table.shape
     with _on(stream, table.device):
-        y = out if out is not None else _rows_like(table, ids.shape[0], table.shape[1], table.dtype)
+        y = out if out is not None else _rows_like(table, n, c, table.dtype)
         lat_embed_fwd(ids, table, scale, pad_id, y, d_status, stream)
     return y
 
@@ -310,13 +312,13 @@ def embed_fwd(ids, table, scale: float = 1.0, pad_id: int = -1, d_status=None, o
 def embed_wgrad(ids, dy, vocab: int, scale: float = 1.0, pad_id: int = -1, ws: Workspace | None = None, d_status=None,
                 out=None, stream=None):
     """The table's gradient (vocab, c) in fp32: scale * the sum of dy's rows of each token."""
+    n, c = dy.shape
     with _on(stream, dy.device):
-        dt = out if out is not None else _rows_like(dy, vocab, dy.shape[1], torch.float32)
+        dt = out if out is not None else _rows_like(dy, vocab, c, torch.float32)
         if dt.shape[0] != vocab:
             raise ValueError(f"out has {dt.shape[0]} rows, not {vocab}")
         ws = ws or Workspace(dy.device)
-        lat_embed_wgrad(ids, dy, scale, pad_id, dt, ws.get(lat_embed_wgrad_ws_bytes(dy.shape[0], vocab, dy.shape[1])),
-                        d_status, stream)
+        lat_embed_wgrad(ids, dy, scale, pad_id, dt, ws.get(lat_embed_wgrad_ws_bytes(n, vocab, c)), d_status, stream)
     return dt
 
 
@@ -368,7 +370,7 @@ def q8_unpack(rows: Q8Rows, dtype: torch.dtype = torch.bfloat16, out=None, strea
 
 def conv_wgrad_q8(x: Q8Rows, dy, kmap: KernelMap, ws: Workspace | None = None, d_status=None, out=None, stream=None):
     """conv_wgrad with the convolution's input rows in 8 bits."""
-    cin, cout = x.q.shape[1], dy.shape[1]
+    (_, cin), (_, cout) = x.q.shape, dy.shape
     with _on(stream, dy.device):
         dw = out if out is not None else dy.new_empty((kmap.k3, cin, cout), dtype=torch.float32)
         ws = ws or Workspace(dy.device)
@@ -401,13 +403,14 @@ def rms_norm_fwd(x, w=None, res=None, eps: float = 1e-6, rows: bool = True, q8: 
 def rms_norm_bwd(dy, h, rstd, w=None, dh=None, want_dw: bool = True, ws: Workspace | None = None, out=None, stream=None):
     """(dx, dw) of rms_norm_fwd from h (rows, or their Q8Rows) and rstd: dx, the gradient of x and of res
     alike, with dh (the gradient that reaches h past the norm) added; dw in fp32, None without ``want_dw``."""
+    n, c = dy.shape
     with _on(stream, dy.device):
         dx = out if out is not None else torch.empty_like(dy)
-        dw = _vector_like(dy, dy.shape[1]) if want_dw else None
+        dw = _vector_like(dy, c) if want_dw else None
         buf = None
         if want_dw:
             ws = ws or Workspace(dy.device)
-            buf = ws.get(lat_rms_norm_bwd_ws_bytes(dy.shape[0], dy.shape[1]))
+            buf = ws.get(lat_rms_norm_bwd_ws_bytes(n, c))
         q = isinstance(h, Q8Rows)
         lat_rms_norm_bwd(dy, dh, None if q else h, h.q if q else None, h.scale if q else None, rstd, w, dx, dw, buf,
                          stream)

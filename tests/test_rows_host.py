@@ -114,6 +114,11 @@ def test_binding_refuses_wrong_tensors(lib):
         _lib.lat_embed_wgrad(ids[:3], x, 1.0, -1, x)
     with pytest.raises(ValueError, match="table"):
         _lib.lat_embed_fwd(ids, x.double(), 1.0, -1, x)
+    for f in (lambda: scv.embed_fwd(ids, x[0]), lambda: scv.embed_fwd(ids[0], x), lambda: scv.embed_wgrad(ids, x[0], 10),
+              lambda: scv.rms_norm_bwd(x[0], x[0], torch.zeros(1)), lambda: scv.rms_norm_fwd(x[0]),
+              lambda: scv.q8_pack(x[None]), lambda: scv.conv_wgrad_q8(scv.Q8Rows(q, s), x[0], None)):
+        with pytest.raises(ValueError):                                             # rows are (n, c), ids (n,)
+            f()
     with pytest.raises(ValueError, match="dtable"):
         _lib.lat_embed_wgrad(ids, x, 1.0, -1, torch.zeros(10, 24))
     with pytest.raises(ValueError, match="res has shape"):
