@@ -687,7 +687,8 @@ constexpr int64_t kFewCounts = 32768;
 // sums' and the join's blocks had taken every SM, and crowded on the first that came free: 443 us
 // for 2,048 rows x 4096, 32,000 tokens, now 107.)
 constexpr size_t kLargeBytes = size_t(16) << 20;
-constexpr int kZeroBlocks = 592;  // 32,768 rows x 512, 131,072 tokens: 85 us with 74 blocks, 80 with 148, 75 with 296, 72 with 592 and more
+// (32,768 rows x 512, 131,072 tokens: 85 us with 74 blocks, 80 with 148, 75 with 296, 72 with 592 and more)
+constexpr int kZeroBlocks = 592;
 constexpr int64_t kSmallWords = 32768;  // of the bitmap that the one-block sort clears itself
 
 // The side stream, or null where there is none to be had: creating it is left to calls outside
@@ -769,7 +770,8 @@ lat_status wgrad(const I *ids, int64_t n, const T *dy, int64_t vocab, int c, flo
             const int to = i & 1;
             Pass p{i ? w.key[1 - to] : nullptr, i ? w.row[1 - to] : nullptr, w.key[to], w.row[to], w.counts,
                    scan ? w.totals : nullptr, w.open_count, n, tiles, i * digit, digit};
-            LAT_CUDA_TRY(launch_pdl(count, dim3(tiles), dim3(kThreads), i ? 0 : seen_bytes(vocab), s, p, d, i ? nullptr : d_status));
+            LAT_CUDA_TRY(launch_pdl(count, dim3(tiles), dim3(kThreads), i ? 0 : seen_bytes(vocab), s, p, d,
+                                    i ? nullptr : d_status));
             if (i == 0 && !joined) {  // the bitmap is complete on s
                 if ((side = free_side_stream(s)) != nullptr) LAT_CUDA_TRY(side_fork(*side, s));
                 const lat_status st = zeros(side ? side->side : s);

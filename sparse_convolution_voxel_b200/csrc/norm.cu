@@ -73,7 +73,8 @@ __global__ void __launch_bounds__(L == 0 ? kWideThreads : kThreads) norm_fwd_ker
     pdl_enter();
     __shared__ float s_sum[2 * kMaxWarps];
     const int lanes = L == 0 ? int(blockDim.x) : L;
-    const int64_t row = L == 0 ? int64_t(blockIdx.x) : blockIdx.x * int64_t(kThreads / (L == 0 ? 1 : L)) + threadIdx.x / lanes;
+    const int64_t row = L == 0 ? int64_t(blockIdx.x)
+                               : blockIdx.x * int64_t(kThreads / (L == 0 ? 1 : L)) + threadIdx.x / lanes;
     const int lane = L == 0 ? int(threadIdx.x) : int(threadIdx.x) % lanes;
     const int slices = a.c / 8;
     Slice8<T> xs[K], rs[K];
@@ -145,8 +146,13 @@ constexpr int ring_bytes(bool dh) {
     return K * (int(8 * sizeof(T)) * (1 + (Q8 ? 0 : 1) + (dh ? 1 : 0)) + (Q8 ? 8 : 0));
 }
 
+template <typename T, int L, int K>
+constexpr int min_blocks() {  // per SM, for the registers: what the ring admits
+    return L > 0 && K == 1 ? 4 : L == 0 && K == 2 && sizeof(T) == 2 ? 2 : 1;
+}
+
 template <typename T, int L, int K, bool Q8>
-__global__ void __launch_bounds__(L == 0 ? kWideThreads : kThreads, L > 0 && K == 1 ? 4 : L == 0 && K == 2 && sizeof(T) == 2 ? 2 : 1)
+__global__ void __launch_bounds__(L == 0 ? kWideThreads : kThreads, min_blocks<T, L, K>())
 norm_bwd_kernel(Bwd<T> a) {
     pdl_enter();
     __shared__ float s_sum[2 * kMaxWarps];

@@ -67,7 +67,8 @@ struct Cfg {
     // Blocks in a group's ring: what shared memory admits.  (A block takes some 3,000 cycles from its gather to its
     // MMAs' end: where the rows lie in L2, the ring's length bounds the rate.)
     static constexpr uint32_t kSlot = kBBytes + kXBytes + kScaleBytes;
-    static constexpr uint32_t kRoom = 232448 - 2048 - 1536 - kGroups * kTiles * kABytes;  // but static variables and barriers
+    // but the static variables (2048) and the barriers with their alignment (1536)
+    static constexpr uint32_t kRoom = 232448 - 2048 - 1536 - kGroups * kTiles * kABytes;
     static constexpr int kRing = kRoom / (kGroups * kSlot) < kMaxRing ? kRoom / (kGroups * kSlot) : kMaxRing;
     static_assert(kRing > kTiles, "a group's ring is longer than its A tiles are many");
     static constexpr uint32_t kDyAt = kGroups * kTiles * kABytes;        // the A tiles, then the dy tiles, raw x, scales
@@ -189,7 +190,8 @@ __device__ __forceinline__ void widen(const uint4 &q, int e, uint4 &lo, uint4 &h
             uint32_t o[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const __half2_raw r = __nv_cvt_fp8x2_to_halfraw2(__nv_fp8x2_storage_t(w[i / 2] >> (16 * (i & 1))), __NV_E4M3);
+                const __half2_raw r =
+                    __nv_cvt_fp8x2_to_halfraw2(__nv_fp8x2_storage_t(w[i / 2] >> (16 * (i & 1))), __NV_E4M3);
                 const __half2 v = __hmul2(__half2(r), s);
                 o[i] = *reinterpret_cast<const uint32_t *>(&v);
             }
@@ -212,7 +214,8 @@ __device__ __forceinline__ void widen(const uint4 &q, int e, uint4 &lo, uint4 &h
 
 template <typename T, int M, int N>
 __global__ void __launch_bounds__(kThreads, 1)
-wgrad_q8_kernel(const __grid_constant__ CUtensorMap dy_map, int centre, const uint8_t *__restrict__ q, const uint8_t *__restrict__ scale, const T *__restrict__ dy,
+wgrad_q8_kernel(const __grid_constant__ CUtensorMap dy_map, int centre, const uint8_t *__restrict__ q,
+                const uint8_t *__restrict__ scale, const T *__restrict__ dy,
                 const int64_t *__restrict__ pair_off, const int32_t *__restrict__ pair_in,
                 const int32_t *__restrict__ pair_out, int64_t capacity, int k3, int64_t n_in, int64_t n_out,
                 float *__restrict__ partial, int32_t *__restrict__ ranges, uint64_t wait_ns, int32_t *d_status) {

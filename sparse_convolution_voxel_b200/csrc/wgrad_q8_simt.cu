@@ -56,8 +56,8 @@ wgrad_q8_simt_kernel(const uint8_t *__restrict__ q, const uint8_t *__restrict__ 
     const int64_t P = s_off[k3];
     const int S = share_count(P, most), v = blockIdx.x;
     if (v == 0 && blockIdx.y == 0 && tid < k3) {
-        // for the reduction, the partials (slot share + offset) of the shares meeting offset tid's pairs [a, b): share v has the pairs
-        // from P v / S, so pair p is in share floor((S (p + 1) - 1) / P)
+        // for the reduction, the partials (slot share + offset) of the shares meeting offset tid's pairs [a, b):
+        // share v has the pairs from P v / S, so pair p is in share floor((S (p + 1) - 1) / P)
         const int64_t a = max(int64_t(0), s_off[tid]), b = min(s_off[tid + 1], P);
         ranges[2 * tid] = a < b ? int((S * (a + 1) - 1) / P) + tid : 0;
         ranges[2 * tid + 1] = a < b ? int((S * b - 1) / P) + tid : -1;
