@@ -678,8 +678,10 @@ static int64_t tiles_of(int64_t n) {
 // Up to this many counts (tiles x digit values) every block of the scatter scans them itself, a
 // launch less in every pass.  These calls wait for their launches: 8,192 rows of 1,000 tokens
 // 25 us, with the scan 28; 24,000 of 50,000 tokens 32, with it 38.  (On the GPU alone 32 tiles x
-// 1024 digit values take 2 us more so, 128 x 512 take 20.)
-constexpr int64_t kFewCounts = 32768;
+// 1024 digit values take 2 us more so, 128 x 512 take 20.)  Beside a large table's zeros, whose
+// writes every read of a count waits behind, fewer: 32,768 rows x 512, 131,072 tokens (64 x 512
+// counts) 78 us, without the scan 121; 16,383 x 1024, 50,257 tokens (32 x 256) 64, without it 63.
+constexpr int64_t kFewCounts = 32768, kFewCountsBeside = 8192;
 
 // Zeros of at least this many bytes have a kernel of their own: with the launches of a sort ahead
 // on the side stream (a fork and a join cost a few microseconds, the zeros of 16 MB as many);
@@ -763,7 +765,8 @@ lat_status wgrad(const I *ids, int64_t n, const T *dy, int64_t vocab, int c, flo
         const int bits = key_bits(vocab), passes = (bits + kMaxBits - 1) / kMaxBits;
         const int digit = std::max(2, (bits + passes - 1) / passes), tiles = int(tiles_of(n));
         const int bins = 1 << digit;
-        const bool few = tile_rounds(n) == 2, scan = int64_t(tiles) * bins > kFewCounts;
+        const bool few = tile_rounds(n) == 2;
+        const bool scan = int64_t(tiles) * bins > (joined ? kFewCounts : kFewCountsBeside);
         auto count = few ? count_kernel<I, 2> : count_kernel<I, 4>;
         auto scatter = few ? scatter_kernel<I, 2> : scatter_kernel<I, 4>;
         for (int i = 0; i < passes; ++i) {
