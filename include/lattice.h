@@ -72,7 +72,7 @@ typedef enum {
     LAT_ERR_CAPACITY = 16,    /* an output buffer is smaller than the result (device)   */
     LAT_ERR_UNSUPPORTED = 32, /* shape / dtype combination not implemented (host)       */
     LAT_ERR_CUDA = 64,        /* a CUDA runtime call failed (host)                      */
-    LAT_ERR_WORKSPACE = 128,  /* ws_bytes smaller than the *_ws_bytes query (host)      */
+    LAT_ERR_WORKSPACE = 128,  /* ws_bytes below the *_ws_bytes query, or ws misaligned (host) */
     LAT_ERR_BAD_MAP = 256,    /* a kernel map holds a row index outside [0, n_in) (device) */
     LAT_ERR_TIMEOUT = 512,    /* a bounded in-kernel wait gave up; the kernel drained and exited */
     LAT_ERR_BAD_ID = 1024     /* a token id is outside [0, vocab) and not the padding id (device) */
@@ -440,8 +440,8 @@ lat_status lat_q8_unpack(const void *q, const void *scale, int64_t n, int32_t c,
 
 /* lat_sconv_wgrad with x (map->n_in, cin) in 8 bits: dW[k] = sum over pairs
  * (i, j) of offset k of (q * scale)[i]^T dy[j], fp32.  dtype is dy's (16-byte
- * aligned, fp32 32); scale 4-byte aligned.  Limits and errors as for
- * lat_sconv_wgrad.  Deterministic in the same way; the number of shares
+ * aligned, fp32 32); scale 4-byte, dw 16-byte and ws 32-byte aligned (another
+ * ws: LAT_ERR_WORKSPACE).  Limits and errors as for lat_sconv_wgrad.  Deterministic in the same way; the number of shares
  * depends on the pair count and the channel counts alone.  In a map of mode
  * LAT_SUBM pair m of the centre offset is (m, m), as lat_kmap_query writes
  * it: those rows are copied by their number, not by the pair list. */

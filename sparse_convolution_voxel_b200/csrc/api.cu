@@ -119,7 +119,8 @@ extern "C" lat_status lat_sconv_wgrad_q8(const void *q, const void *scale, int32
         !aligned16(dw))
         return LAT_ERR_ARG;
     if (map->pair_capacity > 0 && (!map->pair_in || !map->pair_out)) return LAT_ERR_ARG;
-    if (!ws || !aligned16(ws) || ws_bytes < lat_sconv_wgrad_q8_ws_bytes(cin, cout, map, dtype))
+    // the partials, at the workspace's beginning, are stored 32 bytes at a time
+    if (!ws || reinterpret_cast<uintptr_t>(ws) % 32 || ws_bytes < lat_sconv_wgrad_q8_ws_bytes(cin, cout, map, dtype))
         return LAT_ERR_WORKSPACE;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     if (dtype != LAT_F32 && wgrad_tc_supported(cin, cout))

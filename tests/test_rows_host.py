@@ -150,3 +150,20 @@ def test_binding_refuses_wrong_tensors(lib):
 def test_status_bit_of_a_bad_id(lib):
     assert scv.lat_status_string(1024) == "token id out of range"
     assert "LAT_ERR_BAD_ID" in str(scv.LatticeError(1024))
+
+
+def _map(n_in=10, n_out=10, capacity=100):
+    km = _lib.lat_kmap()
+    km.k3, km.n_out, km.n_in, km.pair_capacity = 27, n_out, n_in, capacity
+    km.nbr, km.perm, km.tile_mask, km.pair_off, km.pair_in, km.pair_out = (P(4096),) * 6
+    return km
+
+
+@pytest.mark.parametrize("cin,cout,dt", [(64, 64, 1), (128, 128, 2), (16, 16, 0), (40, 24, 2)])
+def test_weight_gradient_from_8bit_rows_refuses_a_misaligned_workspace(lib, cin, cout, dt):
+    """The partials are stored 32 bytes at a time, from the workspace's beginning."""
+    km = _map()
+    need = lib.lat_sconv_wgrad_q8_ws_bytes(cin, cout, ctypes.byref(km), dt)
+    for off in (4, 8, 16, 24, 48):
+        assert lib.lat_sconv_wgrad_q8(A, B, cin, C, cout, ctypes.byref(km), P(16384), dt, P((1 << 20) + off), need + 64,
+                                      None, None) == WORKSPACE, off
