@@ -113,7 +113,7 @@ extern "C" lat_status lat_sconv_wgrad_q8(const void *q, const void *scale, int32
     using namespace lat;
     if (!map_ok(map) || !chan_ok(cin, dtype) || !chan_ok(cout, dtype) || !dw || !map->pair_off) return LAT_ERR_ARG;
     if (dtype != LAT_F32 && dtype != LAT_F16 && dtype != LAT_BF16) return LAT_ERR_ARG;
-    if (map->n_in > 0 && (!q || !scale)) return LAT_ERR_ARG;
+    if ((map->n_in > 0 && (!q || !scale)) || (map->n_out > 0 && !dy)) return LAT_ERR_ARG;
     const uintptr_t slice = dtype == LAT_F32 ? 32 : 16;
     if (!aligned16(q) || reinterpret_cast<uintptr_t>(scale) % 4 || reinterpret_cast<uintptr_t>(dy) % slice ||
         !aligned16(dw))

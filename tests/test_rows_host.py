@@ -167,3 +167,9 @@ def test_weight_gradient_from_8bit_rows_refuses_a_misaligned_workspace(lib, cin,
     for off in (4, 8, 16, 24, 48):
         assert lib.lat_sconv_wgrad_q8(A, B, cin, C, cout, ctypes.byref(km), P(16384), dt, P((1 << 20) + off), need + 64,
                                       None, None) == WORKSPACE, off
+
+
+@pytest.mark.parametrize("cin,cout,dt", [(64, 64, 1), (16, 16, 0)])
+def test_weight_gradient_from_8bit_rows_refuses_null_gradient_rows(lib, cin, cout, dt):
+    assert lib.lat_sconv_wgrad_q8(A, B, cin, None, cout, ctypes.byref(_map()), P(16384), dt, P(1 << 20), 1 << 30, None,
+                                  None) == ARG
