@@ -78,6 +78,9 @@ struct Cfg {
     static constexpr uint32_t kSmem = kBars + 512 + 1024;
     static constexpr uint32_t kTmemCols = 4 * N;  // the groups' accumulators and the total; a power of two
     static constexpr int kChunks = M / 64;  // 16-byte raw chunks per thread and block
+    // arrivals that a slot's copies take: the load thread, the gathering threads' copies and, where they store s_odd,
+    // their warps
+    static constexpr uint32_t kLandings = 1 + kGatherThreads + (M == 64 ? kGatherWarps : 0);
 };
 template <typename T, int M, int N> struct KernelTag {};  // one launch-config cache per kernel
 
@@ -248,7 +251,7 @@ wgrad_q8_kernel(const __grid_constant__ CUtensorMap dy_map, int centre, const ui
             ptx::mbar_init(&accempty[s], kEpiWarps * 32);
         }
         for (int s = 0; s < kGroups * kRing; ++s) {
-            ptx::mbar_init(&landed[s], 1 + kGatherThreads);
+            ptx::mbar_init(&landed[s], C::kLandings);
             ptx::mbar_init(&freed[s], 1);
             s_last[s] = -1;
         }
@@ -448,6 +451,11 @@ wgrad_q8_kernel(const __grid_constant__ CUtensorMap dy_map, int centre, const ui
                 }
             }
             ptx::cp_async_arrive_noinc(&landed[r]);  // when this thread's copies are there
+            if (M == 64) {
+                // that arrival stands for the copies alone: the warp's stores to s_odd are released by one of their own
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(&landed[r]);
+            }
             if (++slot == kRing) {
                 slot = 0;
                 phase ^= 1;

@@ -411,6 +411,30 @@ def test_weight_gradient_of_a_map_that_is_mostly_centre(n, cin, cout, dtype):
     assert torch.equal(scv.conv_wgrad_q8(scv.Q8Rows(r.q, odd), dy, km), dw)
 
 
+@pytest.mark.parametrize("cin,cout,dtype", [(64, 64, torch.bfloat16), (64, 128, torch.float16), (128, 64, torch.bfloat16)])
+def test_weight_gradient_of_rows_with_scales_of_their_own(cin, cout, dtype):
+    """Neighbouring rows, and neighbouring groups of a row, whose scales are powers of two apart: a pair that took
+    another one's scale byte would be off by its factor.  Called many times, the bits stay."""
+    coords = rand_coords(np.random.default_rng(11), 9001, -12, 12)
+    km, nbr = _subm(coords)
+    n = len(coords)
+    factor = 2.0 ** ((torch.arange(n)[:, None] * 5 + torch.arange(cin) // 32 * 3) % 13 - 6).cuda()
+    r = scv.q8_pack((_rand(3, n, cin) * factor).to(dtype))
+    dy = _rand(4, n, cout, dtype=dtype)
+    st = scv.new_status()
+    dw = scv.conv_wgrad_q8(r, dy, km, d_status=st)
+    scv.check_status(st)
+    x, g = values_q8(r), dy.double()
+    for k in range(27):
+        j = np.nonzero(nbr[:, k] >= 0)[0]
+        i, j = torch.from_numpy(nbr[j, k].astype(np.int64)).cuda(), torch.from_numpy(j).cuda()
+        ref, mag = x[i].t() @ g[j], x[i].abs().t() @ g[j].abs()
+        _within(dw[k], ref, (2048 + 64) * 2.0 ** -23 * mag, f"offset {k}")
+    ws = scv.Workspace()
+    for _ in range(50):
+        assert torch.equal(dw, scv.conv_wgrad_q8(r, dy, km, ws))
+
+
 def test_weight_gradient_wait_that_runs_out():
     """With no time to wait the kernel gives up, says so and leaves the GPU in order: the next call is right."""
     coords = rand_coords(np.random.default_rng(6), 5000, -12, 12)
