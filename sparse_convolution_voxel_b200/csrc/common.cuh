@@ -284,6 +284,27 @@ inline cudaError_t side_join(SideStream &ss, cudaStream_t s) {
     return e == cudaSuccess ? cudaStreamWaitEvent(s, ss.join_ev, 0) : e;
 }
 
+// A fork that is joined on every way out of an entry point, a failed launch's too: join() at its end gives the join's
+// own error, and what is still open after that the destructor joins.
+struct SideScope {
+    cudaStream_t s;
+    SideStream *forked = nullptr;
+    explicit SideScope(cudaStream_t s_) : s(s_) {}
+    SideScope(const SideScope &) = delete;
+    SideScope &operator=(const SideScope &) = delete;
+    ~SideScope() { join(); }
+    cudaError_t fork(SideStream &side) {
+        const cudaError_t e = side_fork(side, s);
+        if (e == cudaSuccess) forked = &side;
+        return e;
+    }
+    cudaError_t join() {
+        SideStream *side = forked;
+        forked = nullptr;
+        return side ? side_join(*side, s) : cudaSuccess;
+    }
+};
+
 // CTAs of a persistent kernel that can be resident at once on the current device.
 // The kernels are compiled with __launch_bounds__(threads, max_per_sm), so
 // registers admit max_per_sm CTAs; shared memory admits

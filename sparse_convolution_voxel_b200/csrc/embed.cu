@@ -740,7 +740,7 @@ lat_status wgrad(const I *ids, int64_t n, const T *dy, int64_t vocab, int c, flo
     const int64_t words = (vocab + 31) / 32;
     const Ids<I> d{ids, vocab, pad, w.present};
     const bool one_block = n <= kSmall && words <= kSmallWords;  // of the sort
-    SideStream *side = nullptr;  // where the zeros of a large table go
+    SideScope beside(s);  // the zeros of a large table
     auto zeros = [&](cudaStream_t to) -> lat_status {
         uint32_t tokens = 32;  // of a warp at a time: some 64 KB of zeros
         while (tokens > 1 && tokens * uint32_t(c) * 4 > 65536) tokens /= 2;
@@ -776,7 +776,8 @@ lat_status wgrad(const I *ids, int64_t n, const T *dy, int64_t vocab, int c, flo
             LAT_CUDA_TRY(launch_pdl(count, dim3(tiles), dim3(kThreads), i ? 0 : seen_bytes(vocab), s, p, d,
                                     i ? nullptr : d_status));
             if (i == 0 && !joined) {  // the bitmap is complete on s
-                if ((side = free_side_stream(s)) != nullptr) LAT_CUDA_TRY(side_fork(*side, s));
+                SideStream *side = free_side_stream(s);
+                if (side) LAT_CUDA_TRY(beside.fork(*side));
                 const lat_status st = zeros(side ? side->side : s);
                 if (st != LAT_OK) return st;
             }
@@ -791,12 +792,12 @@ lat_status wgrad(const I *ids, int64_t n, const T *dy, int64_t vocab, int c, flo
         Runs p{w.key[at], w.row[at], uint32_t(n), uint32_t(vocab), 0, run_shares(n, c), c, scale, w.head, w.tail, w.open,
                w.open_count, w.last, dtable, joined ? w.present : nullptr};
         p.share = uint32_t((n + p.shares - 1) / p.shares);
-        const int groups = kThreads / lanes_of(c), slabs = (c / 8 + 31) / 32, beside = std::min(slabs, groups);
-        const int per_block = groups / beside;
+        const int groups = kThreads / lanes_of(c), slabs = (c / 8 + 31) / 32, abreast = std::min(slabs, groups);
+        const int per_block = groups / abreast;
         const lat_status st = by_lanes(c, [&](auto l) -> lat_status {
             constexpr int L = decltype(l)::value;
-            const dim3 grid(unsigned((p.shares + per_block - 1) / per_block), unsigned((slabs + beside - 1) / beside));
-            LAT_CUDA_TRY(launch_pdl(sums_kernel<T, L>, grid, dim3(unsigned(L * beside * per_block)), 0, s, p, dy,
+            const dim3 grid(unsigned((p.shares + per_block - 1) / per_block), unsigned((slabs + abreast - 1) / abreast));
+            LAT_CUDA_TRY(launch_pdl(sums_kernel<T, L>, grid, dim3(unsigned(L * abreast * per_block)), 0, s, p, dy,
                                     per_block));
             return LAT_OK;
         });
@@ -805,7 +806,7 @@ lat_status wgrad(const I *ids, int64_t n, const T *dy, int64_t vocab, int c, flo
         LAT_CUDA_TRY(launch_pdl(join_kernel, dim3(unsigned(joined ? most : std::min(p.shares, most)), unsigned(cols)),
                                 dim3(32, kJoinRows), 0, s, p, per_block));
     }
-    if (side) LAT_CUDA_TRY(side_join(*side, s));
+    LAT_CUDA_TRY(beside.join());
     return LAT_OK;
 }
 
