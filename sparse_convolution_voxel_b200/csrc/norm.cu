@@ -146,6 +146,20 @@ constexpr int ring_bytes(bool dh) {
     return K * (int(8 * sizeof(T)) * (1 + (Q8 ? 0 : 1) + (dh ? 1 : 0)) + (Q8 ? 8 : 0));
 }
 
+// Shared memory of a call: the ring, and in its place at the end the groups' sums of dw.
+template <typename T, int L, int K, bool Q8>
+constexpr size_t bwd_smem(bool dh, int threads, int c) {
+    const size_t ring = size_t(ring_bytes<T, K, Q8>(dh)) * size_t(threads) * ring_rows<T, L, K>();
+    const size_t sums = L == 0 ? 0 : sizeof(float) * size_t(kThreads / (L == 0 ? 1 : L)) * size_t(c);
+    return ring > sums ? ring : sums;
+}
+// Most that any call of the kernel takes: its limit is the same in every call, since another host thread may be about
+// to launch it with more than this one.
+template <typename T, int L, int K, bool Q8>
+constexpr size_t bwd_smem_limit() {
+    return bwd_smem<T, L, K, Q8>(true, L == 0 ? kWideThreads : kThreads, 8 * L * K);
+}
+
 template <typename T, int L, int K>
 constexpr int min_blocks() {  // per SM, for the registers: what the ring admits
     return L > 0 && K == 1 ? 4 : L == 0 && K == 2 && sizeof(T) == 2 ? 2 : 1;
@@ -426,15 +440,16 @@ lat_status bwd(const void *dy, const void *dh, const void *h, const void *h8, co
     const int64_t blocks = shares(n, c);
     const lat_status st = by_layout(c, false, [&](auto l, auto k, int threads) -> lat_status {
         constexpr int L = decltype(l)::value, K = decltype(k)::value;
-        auto go = [&](auto kern, size_t row_bytes) -> lat_status {
-            const size_t sums = L == 0 ? 0 : sizeof(float) * size_t(kThreads / (L == 0 ? 1 : L)) * size_t(c);
-            const size_t smem = std::max(sums, row_bytes * size_t(threads) * ring_rows<T, L, K>());
-            LAT_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)));
-            LAT_CUDA_TRY(launch_pdl(kern, dim3(unsigned(blocks)), dim3(threads), smem, s, a));
+        auto go = [&](auto q8) -> lat_status {
+            constexpr bool Q8 = decltype(q8)::value;
+            auto kern = norm_bwd_kernel<T, L, K, Q8>;
+            LAT_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                              int(bwd_smem_limit<T, L, K, Q8>())));
+            LAT_CUDA_TRY(launch_pdl(kern, dim3(unsigned(blocks)), dim3(threads),
+                                    bwd_smem<T, L, K, Q8>(dh != nullptr, threads, c), s, a));
             return LAT_OK;
         };
-        return h8 ? go(norm_bwd_kernel<T, L, K, true>, ring_bytes<T, K, true>(dh != nullptr))
-                  : go(norm_bwd_kernel<T, L, K, false>, ring_bytes<T, K, false>(dh != nullptr));
+        return h8 ? go(std::true_type{}) : go(std::false_type{});
     });
     if (st != LAT_OK || !dw) return st;
     LAT_CUDA_TRY(launch_pdl(norm_dw_kernel, dim3(unsigned((c + 31) / 32)), dim3(32, 32), 0, s, partial, int(blocks), c,

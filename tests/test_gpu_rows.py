@@ -315,6 +315,34 @@ def test_norm_gradient(dtype, n, c, saved):
         assert got is a and torch.equal(a, dx)
 
 
+def test_norm_gradients_from_two_host_threads():
+    """One thread's rows have another gradient added, which takes more shared memory of the same kernel; none of the
+    calls fails."""
+    rows = [[_rand(i, 8, 8192, dtype=torch.bfloat16) for i in range(k, k + 3)] for k in (0, 10)]
+    f = [scv.rms_norm_fwd(r[0]) for r in rows]
+    want = [scv.rms_norm_bwd(r[1], x.h, x.rstd, dh=d)[0] for r, x, d in zip(rows, f, (None, rows[1][2]))]
+    torch.cuda.synchronize()
+    wrong = []
+
+    def calls(k):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(400):
+                    dx, _ = scv.rms_norm_bwd(rows[k][1], f[k].h, f[k].rstd, dh=rows[1][2] if k else None, want_dw=False)
+                torch.cuda.current_stream().synchronize()
+            if not torch.equal(dx, want[k]):
+                wrong.append("another result")
+        except Exception as e:
+            wrong.append(repr(e))
+
+    threads = [threading.Thread(target=calls, args=(k,)) for k in (0, 1)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong
+
+
 def test_norm_gradient_against_differences():
     """Central differences of L = sum(y a) + sum(h b), in 64 bits with step d: their own error is at most
     d^2 times the third derivative, far below the fp32 bound used here."""

@@ -72,3 +72,26 @@ def test_a_failed_call_leaves_no_work_behind_on_the_side_stream(fake, n, vocab, 
         assert len(joined) == 1 and len(records) == 1, f"call {fail} of {len(made)}"
         assert got[records[0]].a == got[joined[0]].b and records[0] < joined[0]
         assert all(m.b == stream for m in got[records[0]:] if m.what == LAUNCH)
+
+
+@pytest.mark.parametrize("q8", [False, True])
+@pytest.mark.parametrize("dtype", [0, 1, 2])
+def test_a_kernels_shared_memory_limit_does_not_change_between_calls(fake, dtype, q8):
+    """Two host threads may call at once: a call that lowered the limit of a kernel that another one is about to launch
+    with more would make that launch fail."""
+    limits = {}
+    h, h8 = (None, P(1 << 21)) if q8 else (P(1 << 21), None)
+    for c in (8, 32, 40, 64, 72, 128, 256, 264, 512, 520, 1024, 1032, 2048, 4096, 5120, 8192, 8200, 12288, 16384):
+        for dh in (None, P(1 << 22)):
+            for dw in (None, P(1 << 23)):
+                status, got = calls(fake, -1, lambda: fake.lat_rms_norm_bwd(
+                    P(1 << 20), dh, h, h8, h8, P(4096), P(8192), 1000, c, P(1 << 24), dw, dtype, P(1 << 25), 1 << 30, None))
+                assert status == OK
+                for m in got:
+                    if m.what == ATTRIBUTE:
+                        limits.setdefault((m.a, m.b), set()).add(m.c)
+                launched = [m for m in got if m.what == LAUNCH]
+                assert len(launched) == (2 if dw else 1)
+                most = max(v for (f, _), vs in limits.items() if f == launched[0].a for v in vs)
+                assert launched[0].c <= most <= 232448 - 1024
+    assert all(len(v) == 1 for v in limits.values()), sorted(map(sorted, limits.values()))
