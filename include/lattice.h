@@ -439,12 +439,17 @@ lat_status lat_q8_unpack(const void *q, const void *scale, int64_t n, int32_t c,
                          lat_stream stream);
 
 /* lat_sconv_wgrad with x (map->n_in, cin) in 8 bits: dW[k] = sum over pairs
- * (i, j) of offset k of (q * scale)[i]^T dy[j], fp32.  dtype is dy's (16-byte
- * aligned, fp32 32); scale 4-byte, dw 16-byte and ws 32-byte aligned (another
- * ws: LAT_ERR_WORKSPACE).  Limits and errors as for lat_sconv_wgrad.  Deterministic in the same way; the number of shares
- * depends on the pair count and the channel counts alone.  In a map of mode
- * LAT_SUBM pair m of the centre offset is (m, m), as lat_kmap_query writes
- * it: those rows are copied by their number, not by the pair list. */
+ * (i, j) of offset k of x[i]^T dy[j], fp32, x the values that lat_q8_unpack
+ * writes in dtype, whatever the channel counts.  So bf16 and fp32 multiply
+ * q * scale itself (bf16: subnormals aside); in fp16 a value below 2^-14 is
+ * rounded to a multiple of 2^-24 and one above 65504 held there, which rows
+ * packed from fp16 lose nothing by: keep the rows of a wider type with dy in
+ * that type.  dtype is dy's (16-byte aligned, fp32 32); scale 4-byte, dw
+ * 16-byte and ws 32-byte aligned (another ws: LAT_ERR_WORKSPACE).  Limits and
+ * errors as for lat_sconv_wgrad.  Deterministic in the same way; the number
+ * of shares depends on the pair count and the channel counts alone.  In a map
+ * of mode LAT_SUBM pair m of the centre offset is (m, m), as lat_kmap_query
+ * writes it: those rows are copied by their number, not by the pair list. */
 size_t lat_sconv_wgrad_q8_ws_bytes(int32_t cin, int32_t cout, const lat_kmap *map, lat_dtype dtype);
 lat_status lat_sconv_wgrad_q8(const void *q, const void *scale, int32_t cin, const void *dy, int32_t cout,
                               const lat_kmap *map, float *dw, lat_dtype dtype, void *ws, size_t ws_bytes,

@@ -369,7 +369,7 @@ def q8_unpack(rows: Q8Rows, dtype: torch.dtype = torch.bfloat16, out=None, strea
 
 
 def conv_wgrad_q8(x: Q8Rows, dy, kmap: KernelMap, ws: Workspace | None = None, d_status=None, out=None, stream=None):
-    """conv_wgrad with the convolution's input rows in 8 bits."""
+    """conv_wgrad with the convolution's input rows in 8 bits, taken as q8_unpack writes them in dy's type."""
     (_, cin), (_, cout) = x.q.shape, dy.shape
     with _on(stream, dy.device):
         dw = out if out is not None else dy.new_empty((kmap.k3, cin, cout), dtype=torch.float32)

@@ -247,6 +247,17 @@ template <> __device__ __forceinline__ float in_range<__half>(float v) {
     return fabsf(v) > 65504.f ? copysignf(65504.f, v) : v;  // NaN stays NaN
 }
 
+// Values of a group with scale byte e as T holds them, back in fp32: only fp16 changes one (bf16 does below 2^-133,
+// which is left), and none of a group with 2^-9 scale, e4m3's smallest step, at least 2^-24 and 448 scale below 65504.
+template <typename T>
+__device__ __forceinline__ void as_held(float (&v)[8], int e) {
+    if constexpr (std::is_same<T, __half>::value) {
+        if (uint32_t(e - 112) <= 134u - 112u) return;
+#pragma unroll
+        for (int c = 0; c < 8; ++c) v[c] = __half2float(__float2half_rn(in_range<T>(v[c])));
+    }
+}
+
 // Host checks of the row-wise entry points.
 constexpr int kMaxChannels = 16384;
 inline bool chan_ok(int c) { return c >= 8 && c % 8 == 0 && c <= kMaxChannels; }

@@ -7,7 +7,7 @@
 // 8-bit rows, so the rows are fetched in 8 bits (half the bytes of the pair's x, which
 // is what the kernel waits for) and widened on the way into the MMA's tile.  A value has
 // 4 significant bits and a power of two: bf16 holds it exactly.  fp16 rounds values below
-// 2^-14 to its subnormals' steps and is held at 65504.
+// 2^-14 to its subnormals' steps and is held at 65504, as lat_q8_unpack writes it.
 //
 // One CTA per SM, every role of its own:
 //   * two groups of eight warps widen the blocks of 64 pairs in turn, each with two A tiles

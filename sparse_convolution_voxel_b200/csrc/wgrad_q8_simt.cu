@@ -1,6 +1,7 @@
 // Per-offset weight gradient from 8-bit input rows on CUDA cores, for fp32 and the channel
 // counts that wgrad_q8.cu's tensor-core tiles do not take: dW[k] = sum over pairs (i, j) of
-// offset k of x[i]^T dy[j], all products and sums in fp32 (FFMA, no TF32).
+// offset k of x[i]^T dy[j], all products and sums in fp32 (FFMA, no TF32).  In fp16, x is rounded
+// to fp16 as on the tensor cores, so that the channel counts do not change what is multiplied.
 //
 // The pair list is cut into shares of at least kSharePairs pairs, at most as many as the
 // shape's grid has; their number depends on the pair count and the shape alone.  A block takes
@@ -114,6 +115,7 @@ wgrad_q8_simt_kernel(const uint8_t *__restrict__ q, const uint8_t *__restrict__ 
             float f[8];
             if (o < kBatch * xg) {
                 rows::q8_to_f(xq[m], xe[m], f);
+                rows::as_held<T>(f, xe[m]);
                 float4 *d = reinterpret_cast<float4 *>(s_x + o * 8);
                 d[0] = make_float4(f[0], f[1], f[2], f[3]);
                 d[1] = make_float4(f[4], f[5], f[6], f[7]);

@@ -400,6 +400,33 @@ def test_weight_gradient_from_8bit_rows(n, cin, cout, dtype):
     assert torch.equal(dw, scv.conv_wgrad_q8(r, dy, km)), "the bits depend on timing"
 
 
+@pytest.mark.parametrize("level", ["low", "high"])
+@pytest.mark.parametrize("packed", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("cin,cout", [(16, 16), (40, 24), (64, 64), (64, 128), (128, 64), (128, 128)])
+def test_weight_gradient_in_fp16_takes_the_rows_as_fp16(cin, cout, packed, level):
+    """Rows from a type of another range: groups whose values lie below fp16's normal numbers (and partly below all of
+    them), or above its largest.  Whatever the channel counts, x is what q8_unpack writes in fp16."""
+    coords = rand_coords(np.random.default_rng(cin + cout), 3000, -8, 8)
+    km, nbr = _subm(coords)
+    n, group = len(coords), torch.arange(cin) // 32
+    power = torch.where(group % 2 == 0, -20, -26) if level == "low" else torch.where(group % 2 == 0, 17, 13)
+    r = scv.q8_pack((_rand(cin, n, cin) * (2.0 ** power).cuda()).to(packed))
+    e = r.scale.int()
+    assert bool((e < 112).all() if level == "low" else (e[:, 0] > 134).all())
+    x = values_q8(r).clamp(-65504.0, 65504.0).to(torch.float16)
+    assert not torch.equal(x.double(), values_q8(r)) and torch.equal(x, scv.q8_unpack(r, torch.float16))
+    dy = _rand(cout, n, cout, dtype=torch.float16)
+    st = scv.new_status()
+    dw = scv.conv_wgrad_q8(r, dy, km, d_status=st)
+    scv.check_status(st)
+    x, g = x.double(), dy.double()
+    for k in range(27):
+        j = np.nonzero(nbr[:, k] >= 0)[0]
+        i, j = torch.from_numpy(nbr[j, k].astype(np.int64)).cuda(), torch.from_numpy(j).cuda()
+        ref, mag = x[i].t() @ g[j], x[i].abs().t() @ g[j].abs()
+        _within(dw[k], ref, (len(j) + 64) * 2.0 ** -23 * mag, f"offset {k}")
+
+
 @pytest.mark.parametrize("cin,cout,dtype", [(64, 64, torch.bfloat16), (128, 64, torch.float16)])
 def test_weight_gradient_of_long_shares(cin, cout, dtype):
     """A million pairs: shares of several thousand pairs of one offset, whose sums leave the accumulator more than once."""
