@@ -443,6 +443,34 @@ def test_weight_gradient_of_long_shares(cin, cout, dtype):
         _within(dw[k], ref, (2048 + 64) * 2.0 ** -23 * mag, f"offset {k}")
 
 
+@pytest.mark.parametrize("cin,cout,dtype", [(64, 64, torch.float16), (128, 128, torch.bfloat16), (64, 128, torch.bfloat16),
+                                            (128, 64, torch.float16)])
+def test_weight_gradient_of_sums_longer_than_an_accumulator_takes(cin, cout, dtype):
+    """A full cube of 48^3 voxels: 2.9 million pairs in 592 shares, each longer than the 64 blocks of 64 pairs after which
+    two groups' accumulators are emptied into the segment's total, so that most segments empty them twice.  With values of
+    one sign a part that was lost or added twice would be some hundredths of the sum, the bound is 2.5e-4 of it."""
+    side = 48
+    coords = np.stack(np.meshgrid(np.zeros(1), *[np.arange(side)] * 3, indexing="ij"), -1).reshape(-1, 4).astype(np.int32)
+    coords = np.ascontiguousarray(coords[np.random.default_rng(12).permutation(len(coords))])
+    km, nbr = _subm(coords)
+    pairs = int((nbr >= 0).sum())
+    assert pairs == (3 * side - 2) ** 3 and pairs // (4 * 148) > 64 * 64
+    n = len(coords)
+    for sign in (False, True):
+        x, g = _rand(1, n, cin, dtype=dtype), _rand(2, n, cout, dtype=dtype)
+        r, dy = scv.q8_pack(x.abs() if sign else x), g.abs() if sign else g
+        st = scv.new_status()
+        dw = scv.conv_wgrad_q8(r, dy, km, d_status=st)
+        scv.check_status(st)
+        x, g = values_q8(r), dy.double()
+        for k in range(27):
+            j = np.nonzero(nbr[:, k] >= 0)[0]
+            i, j = torch.from_numpy(nbr[j, k].astype(np.int64)).cuda(), torch.from_numpy(j).cuda()
+            ref, mag = x[i].t() @ g[j], x[i].abs().t() @ g[j].abs()
+            _within(dw[k], ref, (2048 + 64) * 2.0 ** -23 * mag, f"offset {k}")
+        assert torch.equal(dw, scv.conv_wgrad_q8(r, dy, km)), "the bits depend on timing"
+
+
 @pytest.mark.parametrize("n", [64, 65, 4999, 30011])
 @pytest.mark.parametrize("cin,cout,dtype", [(64, 128, torch.bfloat16), (128, 64, torch.float16)])
 def test_weight_gradient_of_a_map_that_is_mostly_centre(n, cin, cout, dtype):
