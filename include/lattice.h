@@ -464,8 +464,8 @@ lat_status lat_sconv_wgrad_q8(const void *q, const void *scale, int32_t cin, con
  * y8_scale, lat_q8_pack's format), h in 8 bits (h8 with h8_scale: what
  * lat_rms_norm_bwd needs), rstd.  Each output is rounded once, from fp32: y
  * and the 8-bit rows do not come from a rounded h.  h may be x or res
- * itself; no other overlap.  eps > 0.  The mean of the squares must be
- * finite in fp32. */
+ * itself; no other overlap.  eps > 0.  The sum of a row's squares must be
+ * finite in fp32 (up to |h| = 10^17 it is, whatever c). */
 lat_status lat_rms_norm_fwd(const void *x, const void *res, const void *w, int64_t n, int32_t c, float eps,
                             void *h, void *y, void *y8, void *y8_scale, void *h8, void *h8_scale,
                             float *rstd, lat_dtype dtype, lat_stream stream);

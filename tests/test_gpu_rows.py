@@ -279,6 +279,25 @@ def test_norm_of_special_rows(dtype):
     assert bool(torch.isfinite(r.y[clean]).all())
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("n,c", [(3, 64), (2, 16384)])
+def test_norm_of_the_largest_rows(dtype, n, c):
+    """Magnitudes up to 10^17, whose squares' sum ends below fp32's largest number at any channel count, both ways."""
+    x, w, dy = (1e17 * (2 * torch.rand(n, c, generator=torch.Generator().manual_seed(c)) - 1)).to(dtype).cuda(), \
+        _rand(c, c, dtype=dtype), _rand(n, n, c, dtype=dtype)
+    x[0] = 9.9e16
+    r = scv.rms_norm_fwd(x, w, q8=True, q8_h=True)
+    h, rstd, y = plain_norm(x, None, w, float(np.float32(1e-6)))
+    _within(r.rstd, rstd, OWN * rstd, "rstd")
+    _within(r.y, y, (UNIT[dtype] + OWN) * y.abs() + TINY[dtype], "y")
+    _check_q8(r.h8, h, 2.0 ** -24, "h in 8 bits")
+    for saved, plain in ((r.h, h), (r.h8, values_q8(r.h8))):
+        dx, dw = scv.rms_norm_bwd(dy, saved, r.rstd, w)
+        ref, own, dw_ref, mag = plain_norm_bwd(dy, plain, r.rstd, w, None)
+        _within(dx, ref, UNIT[dtype] * (ref.abs() + own) + own + TINY[dtype], "dx")
+        _within(dw, dw_ref, 128 * 2.0 ** -24 * mag, "dw")
+
+
 def plain_norm_bwd(dy, h, rstd, w, dh):
     """dx, its bound without the output's rounding, dw and the magnitudes of its terms, in 64 bits."""
     dy, h, r = dy.double(), h.double(), rstd.double()[:, None]
