@@ -406,7 +406,10 @@ lat_status lat_to_dense(const int32_t *coords, int64_t n, const void *feats, int
  * 16 MB and more writes its zeros on a stream of the calling thread's own,
  * between an event that `stream` records and one that it waits for; the
  * thread's first such call outside a capture creates it, and a capture
- * before that goes without. */
+ * before that goes without.  Such calls of one thread on several streams so
+ * follow one another in part: a later one's zeros, for which its stream
+ * waits, are queued behind an earlier one's, which wait for the work in front
+ * of them on their own stream. */
 lat_status lat_embed_fwd(const void *ids, int32_t id_bytes, int64_t n, const void *table, int64_t vocab,
                          int32_t c, float scale, int64_t pad_id, void *y, lat_dtype dtype,
                          int32_t *d_status, lat_stream stream);

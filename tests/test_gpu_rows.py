@@ -732,6 +732,45 @@ def test_two_streams_at_once():
         assert all(torch.equal(g, want[k]) for g in got[k])
 
 
+@pytest.mark.parametrize("in_threads", [False, True])
+def test_gradients_of_large_tables_on_two_streams_at_once(in_threads):
+    """From one host thread they share its side stream, from two each has its own; outputs of a call that follows on
+    the same stream are not overwritten by zeros that are still on their way."""
+    vocab = 40000
+    ids = [_ids(20 + i, n, vocab, torch.int64) for i, n in enumerate((9000, 30000))]
+    dy = [_rand(20 + i, len(d), 128, dtype=torch.bfloat16) for i, d in enumerate(ids)]
+    want = [scv.embed_wgrad(i, d, vocab) for i, d in zip(ids, dy)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    same = [[], []]
+
+    def calls(k):
+        with torch.cuda.stream(streams[k]):
+            ws, out = scv.Workspace(), torch.empty(vocab, 128, device="cuda")
+            for _ in range(6):
+                scv.embed_wgrad(ids[k], dy[k], vocab, ws=ws, out=out.fill_(float("nan")))
+                same[k].append((out == want[k]).all())
+            streams[k].synchronize()
+
+    if in_threads:
+        threads = [threading.Thread(target=calls, args=(k,)) for k in (0, 1)]
+        for t in threads:
+            t.start()
+        for t in threads:
+            t.join()
+    else:
+        for k in (0, 1, 0):
+            calls(k)
+        ws, out = [scv.Workspace() for _ in range(2)], [torch.empty(vocab, 128, device="cuda") for _ in range(2)]
+        torch.cuda.synchronize()
+        for _ in range(6):
+            for k in (0, 1):
+                scv.embed_wgrad(ids[k], dy[k], vocab, ws=ws[k], out=out[k], stream=streams[k])
+        torch.cuda.synchronize()
+        assert all(torch.equal(o, w) for o, w in zip(out, want))
+    assert all(len(v) >= 6 and all(v) for v in same)
+
+
 def test_rows_past_32_bit_offsets():
     """More than 2^31 values: the last rows come out as on their own."""
     n, c = (1 << 31) // 8192 + 40, 8192
