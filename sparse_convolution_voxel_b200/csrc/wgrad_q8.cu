@@ -2,8 +2,8 @@
 // of offset k of x[i]^T dy[j], x in e4m3 with a power-of-two scale per 32 channels, dy in
 // fp16 / bf16, fp32 accumulate in TMEM, fp32 out.
 //
-// The GEMM, its tiles, the shares of the pair list and the partials are those of
-// wgrad_tc.cu.  What differs is the way of x: tcgen05 multiplies 8-bit rows only with
+// The GEMM and its tiles are those of wgrad_tc.cu; the cut of the pair list is its own (kWorkers,
+// Work).  What differs most is the way of x: tcgen05 multiplies 8-bit rows only with
 // 8-bit rows, so the rows are fetched in 8 bits (half the bytes of the pair's x, which
 // is what the kernel waits for) and widened on the way into the MMA's tile.  A value has
 // 4 significant bits and a power of two: bf16 holds it exactly.  fp16 rounds values below

@@ -47,6 +47,64 @@ struct Cfg {
 
 template <typename T, int M, int N> struct KernelTag {};  // one launch-config cache per kernel
 
+// Clamped pair offsets of the k3 offsets (off[k3] = P) into shared memory; one warp.
+__device__ __forceinline__ void load_offsets(const int64_t *pair_off, int64_t capacity, int k3, int64_t *off) {
+    for (int e = threadIdx.x & 31; e <= k3; e += 32) off[e] = min(pair_off[e], capacity);
+}
+
+// Shares of a list of P pairs: min(kWorkers, P), so that no share is empty
+// (every share then writes the partials its slots stand for).
+__device__ __forceinline__ int share_count(int64_t P) { return int(min(int64_t(kWorkers), P)); }
+
+// Share v of the pair list: pairs [P v / S, P (v+1) / S), S = share_count(P).
+__device__ __forceinline__ int64_t share_lo(int64_t P, int v) { return P * v / share_count(P); }
+
+// The share holding pair `pair` (largest v with share_lo(P, v) <= pair); a binary search.
+__device__ __forceinline__ int share_of(int64_t P, int64_t pair) {
+    int lo = 0, hi = share_count(P) - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (share_lo(P, mid) <= pair) lo = mid;
+        else hi = mid - 1;
+    }
+    return lo;
+}
+
+// The segments of this CTA's shares, in order: share v = blockIdx.x, +gridDim.x,
+// ..., and within a share the offsets its range meets.  Every role walks the
+// same sequence.
+struct Segments {
+    const int64_t *off;
+    int k3;
+    int64_t P;
+    int v, k;
+    int64_t hv;
+    __device__ Segments(const int64_t *o, int k3_) : off(o), k3(k3_), P(o[k3_]), v(int(blockIdx.x) - int(gridDim.x)),
+                                                   k(k3_), hv(0) {}
+    // next segment: offset ko, pairs [lo, hi), partial slot
+    __device__ bool next(int &ko, int64_t &lo, int64_t &hi, int &slot) {
+        for (;;) {
+            while (k < k3 && off[k] < hv) {
+                const int64_t a = max(share_lo(P, v), off[k]), b = min(hv, off[k + 1]);
+                const int kk = k++;
+                if (a < b) {
+                    ko = kk;
+                    lo = a;
+                    hi = b;
+                    slot = v + kk;
+                    return true;
+                }
+            }
+            v += gridDim.x;
+            if (v >= share_count(P)) return false;
+            const int64_t wl = share_lo(P, v);
+            hv = share_lo(P, v + 1);
+            k = 0;
+            while (k < k3 && off[k + 1] <= wl) ++k;
+        }
+    }
+};
+
 template <typename T, int M, int N>
 __global__ void __launch_bounds__(kThreads, 2)
 wgrad_tc_kernel(const T *__restrict__ x, const T *__restrict__ dy, const int64_t *__restrict__ pair_off,
@@ -77,8 +135,8 @@ wgrad_tc_kernel(const T *__restrict__ x, const T *__restrict__ dy, const int64_t
         if (blockIdx.x == 0 && lane < k3) {
             // for the reduce: the shares meeting offset lane's pairs [a, b)
             const int64_t P = s_off[k3], a = s_off[lane], b = s_off[lane + 1];
-            ranges[2 * lane] = a < b ? share_of<kWorkers>(P, a) : 0;
-            ranges[2 * lane + 1] = a < b ? share_of<kWorkers>(P, b - 1) : -1;
+            ranges[2 * lane] = a < b ? share_of(P, a) : 0;
+            ranges[2 * lane + 1] = a < b ? share_of(P, b - 1) : -1;
         }
     }
     if (tid == 0) {
@@ -110,7 +168,7 @@ wgrad_tc_kernel(const T *__restrict__ x, const T *__restrict__ dy, const int64_t
         uint32_t it = 0;
         bool ok = true;
         const int g = lane >> 3, c = lane & 7;
-        Segments<kWorkers> seg(s_off, k3);
+        Segments seg(s_off, k3);
         int k, slot;
         int64_t lo, hi;
         while (ok && seg.next(k, lo, hi, slot)) {
@@ -171,7 +229,7 @@ wgrad_tc_kernel(const T *__restrict__ x, const T *__restrict__ dy, const int64_t
         const bool has_row = M == 128 || lane < 16;
         uint32_t ta = 0;
         bool ok = true;
-        Segments<kWorkers> seg(s_off, k3);
+        Segments seg(s_off, k3);
         int k, slot;
         int64_t lo, hi;
         while (ok && seg.next(k, lo, hi, slot)) {
@@ -215,7 +273,7 @@ wgrad_tc_kernel(const T *__restrict__ x, const T *__restrict__ dy, const int64_t
         // ------------------------------------------------------------ MMA issue
         uint32_t it = 0, ta = 0;
         bool ok = true;
-        Segments<kWorkers> seg(s_off, k3);
+        Segments seg(s_off, k3);
         int k, slot;
         int64_t lo, hi;
         while (ok && seg.next(k, lo, hi, slot)) {
