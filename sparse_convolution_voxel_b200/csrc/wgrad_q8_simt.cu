@@ -7,9 +7,9 @@
 // shape's grid has; their number depends on the pair count and the shape alone.  A block takes
 // a share and a 64 x 64 piece of dW[k] (input channels x output channels).  For every 64 pairs
 // of a segment (the share's pairs of one offset) it widens the piece's x and dy into shared
-// memory, and each thread adds 8 x 4 products of the pairs of its group: a piece of fewer than
-// 256 such tiles leaves threads for several groups, which take the pairs in turn and are added
-// in group order at the segment's end.  One fp32 partial per segment; wgrad_q8.cu's reduction
+// memory, and each thread adds 8 x 4 products of the pairs of its group: a piece has at most 128
+// such tiles, so that the block has two groups and more, which take the pairs in turn and are
+// added in group order at the segment's end.  One fp32 partial per segment; wgrad_q8.cu's reduction
 // adds the partials in share order.
 //
 // A small map is bound by the chain of dependent reads (offsets, pairs, rows): few long
@@ -69,6 +69,7 @@ wgrad_q8_simt_kernel(const uint8_t *__restrict__ q, const uint8_t *__restrict__ 
     const int tiles = (M / kTileM) * (N / 4);
     int lanes = 2;  // threads of a group
     while (lanes < tiles) lanes *= 2;
+    static_assert(2 * (kPiece / kTileM) * (kPiece / 4) <= kThreads, "two groups at least");
     const int groups = kThreads / lanes, group = tid / lanes, tile = tid % lanes;
     const bool has_tile = tile < tiles;
     const int ti = has_tile ? tile / (N / 4) * kTileM : 0, tj = has_tile ? tile % (N / 4) * 4 : 0;
@@ -162,28 +163,24 @@ wgrad_q8_simt_kernel(const uint8_t *__restrict__ q, const uint8_t *__restrict__ 
             }
             __syncthreads();
         }
-        // the groups' sums meet in shared memory: [group][M][N], in the rows' place
-        float *sums = groups > 1 ? s_x : nullptr;  // groups * M * N <= kThreads * 32 floats
-        float *out = partial + int64_t(v + k) * cin * cout + int64_t(ci0) * cout + co0;
+        // the groups' sums meet in shared memory, in the rows' place: [group][M][N], at most kThreads * 32 floats
         if (has_tile) {
 #pragma unroll
             for (int a = 0; a < kTileM; ++a) {
-                float4 *d = reinterpret_cast<float4 *>(sums ? sums + (group * M + ti + a) * N + tj
-                                                            : out + int64_t(ti + a) * cout + tj);
+                float4 *d = reinterpret_cast<float4 *>(s_x + (group * M + ti + a) * N + tj);
                 const float2 *r = acc[a / 2];
                 *d = a & 1 ? make_float4(r[0].y, r[1].y, r[2].y, r[3].y) : make_float4(r[0].x, r[1].x, r[2].x, r[3].x);
             }
         }
-        if (sums) {
-            __syncthreads();
-            for (int e = tid; e < M * N; e += kThreads) {
-                float t = 0.f;
-#pragma unroll 8
-                for (int g = 0; g < groups; ++g) t += sums[g * M * N + e];
-                out[int64_t(e / N) * cout + e % N] = t;
-            }
-            __syncthreads();
+        __syncthreads();
+        float *out = partial + int64_t(v + k) * cin * cout + (ci0 * cout + co0);
+        for (int e = tid; e < M * N; e += kThreads) {
+            float t = 0.f;
+#pragma unroll 4
+            for (int g = 0; g < groups; ++g) t += s_x[g * M * N + e];
+            out[e / N * cout + e % N] = t;
         }
+        __syncthreads();
         lo = end;
         ++k;
         while (k < k3 && s_off[k + 1] <= lo) ++k;
