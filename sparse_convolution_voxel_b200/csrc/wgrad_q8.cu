@@ -57,32 +57,8 @@ constexpr int kGatherAt = kWideWarps + kEpiWarps;  // first gathering warp
 constexpr int kMmaWarp = kGatherAt + kGroups * kGatherWarps, kLoadWarp = kMmaWarp + kGroups;
 constexpr int kThreads = (kLoadWarp + 1) * 32;
 constexpr int kWidePairs = kKP / kGroupWarps, kGatherPairs = kKP / kGatherWarps;  // of a block, per warp
+constexpr uint32_t kMaxSmem = 232448, kBarBytes = 512, kAlign = 1024;  // of a CTA; its barriers; the tiles' alignment
 constexpr uint64_t kDrainNs = 1000000000ull;  // limit of the waits that drain a CTA that gave up
-
-template <int M, int N>
-struct Cfg {
-    static constexpr uint32_t kABytes = uint32_t(M) * 128;  // 64 pairs x M channels x 2 bytes
-    static constexpr uint32_t kBBytes = uint32_t(N) * 128;
-    static constexpr uint32_t kXBytes = uint32_t(M) * 64;   // raw
-    // Blocks in a group's ring: what shared memory admits.  (A block takes some 3,000 cycles from its gather to its
-    // MMAs' end: where the rows lie in L2, the ring's length bounds the rate.)
-    static constexpr uint32_t kSlot = kBBytes + kXBytes + kScaleBytes;
-    // but the static variables (2048) and the barriers with their alignment (1536)
-    static constexpr uint32_t kRoom = 232448 - 2048 - 1536 - kGroups * kTiles * kABytes;
-    static constexpr int kRing = kRoom / (kGroups * kSlot) < kMaxRing ? kRoom / (kGroups * kSlot) : kMaxRing;
-    static_assert(kRing > kTiles, "a group's ring is longer than its A tiles are many");
-    static constexpr uint32_t kDyAt = kGroups * kTiles * kABytes;        // the A tiles, then the dy tiles, raw x, scales
-    static constexpr uint32_t kRawAt = kDyAt + kGroups * kRing * kBBytes;
-    static constexpr uint32_t kScaleAt = kRawAt + kGroups * kRing * kXBytes;
-    static constexpr uint32_t kBars = kScaleAt + kGroups * kRing * kScaleBytes;
-    static constexpr uint32_t kSmem = kBars + 512 + 1024;
-    static constexpr uint32_t kTmemCols = 4 * N;  // the groups' accumulators and the total; a power of two
-    static constexpr int kChunks = M / 64;  // 16-byte raw chunks per thread and block
-    // arrivals that a slot's copies take: the load thread, the gathering threads' copies and, where they store s_odd,
-    // their warps
-    static constexpr uint32_t kLandings = 1 + kGatherThreads + (M == 64 ? kGatherWarps : 0);
-};
-template <typename T, int M, int N> struct KernelTag {};  // one launch-config cache per kernel
 
 // A worker's pairs of one offset in one of its shares, in the order in which it takes them.
 // Segments of one offset that follow one another are one sum: one partial.
@@ -150,6 +126,41 @@ struct Work {
         if (lane == 0) count = n;
     }
 };
+
+// A CTA's static shared memory.
+struct Static {
+    Work work;
+    uint8_t odd[kGroups * kMaxRing][kKP];  // M = 64: the pair's scale bytes are the upper half of their word
+    int last[kGroups * kMaxRing];          // parity of the slot's phase if its last block is a run, else -1
+    int run[kGroups * kMaxRing];           // the block is a run: where its scale bytes begin, else -1
+    int abort;
+};
+
+template <int M, int N>
+struct Cfg {
+    static constexpr uint32_t kABytes = uint32_t(M) * 128;  // 64 pairs x M channels x 2 bytes
+    static constexpr uint32_t kBBytes = uint32_t(N) * 128;
+    static constexpr uint32_t kXBytes = uint32_t(M) * 64;   // raw
+    // Blocks in a group's ring: what shared memory admits.  (A block takes some 3,000 cycles from its gather to its
+    // MMAs' end: where the rows lie in L2, the ring's length bounds the rate.)
+    static constexpr uint32_t kSlot = kBBytes + kXBytes + kScaleBytes;
+    static constexpr uint32_t kRoom = kMaxSmem - uint32_t(sizeof(Static)) - kBarBytes - kAlign - kGroups * kTiles * kABytes;
+    static constexpr int kRing = kRoom / (kGroups * kSlot) < kMaxRing ? kRoom / (kGroups * kSlot) : kMaxRing;
+    static_assert(kRing > kTiles, "a group's ring is longer than its A tiles are many");
+    static constexpr uint32_t kDyAt = kGroups * kTiles * kABytes;        // the A tiles, then the dy tiles, raw x, scales
+    static constexpr uint32_t kRawAt = kDyAt + kGroups * kRing * kBBytes;
+    static constexpr uint32_t kScaleAt = kRawAt + kGroups * kRing * kXBytes;
+    static constexpr uint32_t kBars = kScaleAt + kGroups * kRing * kScaleBytes;
+    static constexpr uint32_t kSmem = kBars + kBarBytes + kAlign;
+    static_assert(kSmem + sizeof(Static) <= kMaxSmem, "a CTA's shared memory");
+    static_assert(8 * (kGroups * (kTiles + 2 + 2 * kRing) + 1) + 4 <= kBarBytes, "the barriers and the TMEM address");
+    static constexpr uint32_t kTmemCols = 4 * N;  // the groups' accumulators and the total; a power of two
+    static constexpr int kChunks = M / 64;  // 16-byte raw chunks per thread and block
+    // arrivals that a slot's copies take: the load thread, the gathering threads' copies and, where they store st.odd,
+    // their warps
+    static constexpr uint32_t kLandings = 1 + kGatherThreads + (M == 64 ? kGatherWarps : 0);
+};
+template <typename T, int M, int N> struct KernelTag {};  // one launch-config cache per kernel
 
 // Walks the blocks of the segments.  A block is a run if its pairs are 64 consecutive rows
 // whose scale bytes (G per row) can be copied from a 16-byte boundary: the full blocks of the
@@ -236,11 +247,8 @@ wgrad_q8_kernel(const __grid_constant__ CUtensorMap dy_map, int centre, const ui
     uint64_t *landed = accempty + kGroups;  // bulk and tensor copies, [group][slot]
     uint64_t *drain = landed + kGroups * kRing;  // tracks the MMAs still in flight when a CTA gives up
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
-    __shared__ int s_abort;
-    __shared__ Work s_work;
-    __shared__ uint8_t s_odd[kGroups * kRing][kKP];  // M = 64: the pair's scale bytes are the upper half of their word
-    __shared__ int s_last[kGroups * kRing];          // parity of the slot's phase if its last block is a run, else -1
-    __shared__ int s_run[kGroups * kRing];           // the block is a run: where its scale bytes begin, else -1
+    __shared__ Static st;
+    Work &s_work = st.work;
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (warp == 1) s_work.make(pair_off, capacity, k3, int(blockIdx.x), blockIdx.x == 0 ? ranges : nullptr);
@@ -253,10 +261,10 @@ wgrad_q8_kernel(const __grid_constant__ CUtensorMap dy_map, int centre, const ui
         for (int s = 0; s < kGroups * kRing; ++s) {
             ptx::mbar_init(&landed[s], C::kLandings);
             ptx::mbar_init(&freed[s], 1);
-            s_last[s] = -1;
+            st.last[s] = -1;
         }
         ptx::mbar_init(drain, kGroups);
-        s_abort = 0;
+        st.abort = 0;
         ptx::fence_mbar_init();
         ptx::fence_proxy_async_smem();
     }
@@ -298,14 +306,14 @@ wgrad_q8_kernel(const __grid_constant__ CUtensorMap dy_map, int centre, const ui
             }
             const uint8_t *xs = smem + C::kRawAt + r * C::kXBytes + (gw * kWidePairs + xg) * M + xc * 16;
             const uint8_t *ss = smem + C::kScaleAt + r * kScaleBytes;
-            const int from = s_run[r];
+            const int from = st.run[r];
             uint8_t *row = smem + t * C::kABytes + mb * 8192 + gw * 1024;  // kWidePairs == 8: one 8-pair atom per warp
 #pragma unroll
             for (int i = 0; i < C::kChunks; ++i) {
                 const int sw = i * XP + xg, p = gw * kWidePairs + sw;
                 const uint4 raw = *reinterpret_cast<const uint4 *>(xs + i * XP * M);
                 // channels 16 xc .. 16 xc + 15
-                const int e = ss[(from >= 0 ? from + p * (M / 32) : p * 4 + (M == 64 ? s_odd[r][p] : 0)) + (xc >> 1)];
+                const int e = ss[(from >= 0 ? from + p * (M / 32) : p * 4 + (M == 64 ? st.odd[r][p] : 0)) + (xc >> 1)];
                 uint4 lo, hi;
                 widen<T>(raw, e, lo, hi);
                 *reinterpret_cast<uint4 *>(row + sw * 128 + ((first ^ sw) << 4)) = turn ? hi : lo;
@@ -319,7 +327,7 @@ wgrad_q8_kernel(const __grid_constant__ CUtensorMap dy_map, int centre, const ui
                 phase ^= 1;
             }
         }
-        if (!ok) s_abort = 1;
+        if (!ok) st.abort = 1;
     } else if (warp < kGatherAt) {
         // ------------------------------------------------------------ epilogue: partial of each segment
         const int quad = warp & 3;
@@ -385,7 +393,7 @@ wgrad_q8_kernel(const __grid_constant__ CUtensorMap dy_map, int centre, const ui
             }
             it += blocks;
         }
-        if (!ok) s_abort = 1;
+        if (!ok) st.abort = 1;
     } else if (warp < kMmaWarp) {
         // ------------------------------------------------------------ gather rows
         constexpr int XL = M / 16, XP = 32 / XL;
@@ -432,7 +440,7 @@ wgrad_q8_kernel(const __grid_constant__ CUtensorMap dy_map, int centre, const ui
                     const int64_t left = n_in * (M / 32) - word;
                     ptx::cp_async4(smem + C::kScaleAt + r * kScaleBytes + p * 4, scale + word,
                                    ri < 0 ? 0u : uint32_t(left < 4 ? left : 4));
-                    if (M == 64) s_odd[r][p] = uint8_t(at & 2);
+                    if (M == 64) st.odd[r][p] = uint8_t(at & 2);
                 }
 #pragma unroll
                 for (int i = 0; i < kGatherPairs / XP; ++i) {
@@ -452,7 +460,7 @@ wgrad_q8_kernel(const __grid_constant__ CUtensorMap dy_map, int centre, const ui
             }
             ptx::cp_async_arrive_noinc(&landed[r]);  // when this thread's copies are there
             if (M == 64) {
-                // that arrival stands for the copies alone: the warp's stores to s_odd are released by one of their own
+                // that arrival stands for the copies alone: the warp's stores to st.odd are released by one of their own
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive(&landed[r]);
             }
@@ -473,7 +481,7 @@ wgrad_q8_kernel(const __grid_constant__ CUtensorMap dy_map, int centre, const ui
             }
         }
         ptx::cp_async_wait<0>();
-        if (!ok) s_abort = 1;
+        if (!ok) st.abort = 1;
     } else if (warp < kLoadWarp) {
         // ------------------------------------------------------------ MMA issue, a thread per group
         if (lane == 0) {
@@ -519,7 +527,7 @@ wgrad_q8_kernel(const __grid_constant__ CUtensorMap dy_map, int centre, const ui
                     if (ok) ptx::umma_commit(&accfull[grp]);
                 }
             }
-            if (!ok) s_abort = 1;
+            if (!ok) st.abort = 1;
         }
     } else if (warp == kLoadWarp && lane == 0) {
         // ------------------------------------------------------------ runs of rows
@@ -537,8 +545,8 @@ wgrad_q8_kernel(const __grid_constant__ CUtensorMap dy_map, int centre, const ui
             if (blk.run) {
                 const int64_t row0 = blk.row0, at = row0 * (M / 32);
                 constexpr uint32_t kBytes = kKP * (M / 32) + 16;
-                s_run[r] = int(at & 15);
-                s_last[r] = int(phase ^ 1);
+                st.run[r] = int(at & 15);
+                st.last[r] = int(phase ^ 1);
                 ptx::mbar_arrive_expect_tx(&landed[r], C::kXBytes + C::kBBytes + kBytes);
                 ptx::bulk_load(smem + C::kRawAt + r * C::kXBytes, q + row0 * M, C::kXBytes, &landed[r]);
                 ptx::bulk_load(smem + C::kScaleAt + r * kScaleBytes, scale + (at & ~int64_t(15)), kBytes, &landed[r]);
@@ -547,8 +555,8 @@ wgrad_q8_kernel(const __grid_constant__ CUtensorMap dy_map, int centre, const ui
                     ptx::tma_load_2d(smem + C::kDyAt + r * C::kBBytes + nb * 8192, &dy_map, &landed[r], nb * 64,
                                      int(row0));
             } else {
-                s_run[r] = -1;
-                s_last[r] = -1;
+                st.run[r] = -1;
+                st.last[r] = -1;
                 ptx::mbar_arrive(&landed[r]);
             }
             if (++grp == kGroups) {
@@ -559,11 +567,11 @@ wgrad_q8_kernel(const __grid_constant__ CUtensorMap dy_map, int centre, const ui
                 }
             }
         }
-        if (!ok) s_abort = 1;
+        if (!ok) st.abort = 1;
     }
 
     __syncthreads();
-    if (s_abort) {
+    if (st.abort) {
         // A role gave up.  Before the CTA releases its TMEM and shared memory, everything still
         // writing into them must land: the gathers have (cp.async.wait_all above); the load
         // thread waits for the run that a slot was given last, and the MMA threads commit every MMA they
@@ -571,7 +579,7 @@ wgrad_q8_kernel(const __grid_constant__ CUtensorMap dy_map, int centre, const ui
         bad |= (tid == 0) ? LAT_ERR_TIMEOUT : 0;
         if (warp == kLoadWarp && lane == 0)
             for (int r = 0; r < kGroups * kRing; ++r)  // (a phase whose gather warps gave up stays open: one limit for all)
-                if (s_last[r] >= 0 && !ptx::mbar_wait(&landed[r], s_last[r], kDrainNs)) break;
+                if (st.last[r] >= 0 && !ptx::mbar_wait(&landed[r], st.last[r], kDrainNs)) break;
         if (warp >= kMmaWarp && warp < kLoadWarp && lane == 0) {
             ptx::umma_commit(drain);
             ptx::mbar_wait(drain, 0, kDrainNs);
