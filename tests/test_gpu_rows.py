@@ -793,6 +793,40 @@ def test_rows_past_32_bit_offsets():
     assert torch.equal(scv.embed_wgrad(rows, x, 50), x[-50:].float())
 
 
+def test_a_gradient_past_32_bit_offsets():
+    """A table of more than 2^31 values: tokens at both ends, and zeros in all the rows between."""
+    vocab, c = (1 << 31) // 8192 + 40, 8192
+    ids = torch.tensor([vocab - 1, 3, vocab - 1, vocab - 40, 0, 3], dtype=torch.int32, device="cuda")
+    dy = _rand(9, 6, c, dtype=torch.bfloat16)
+    for rows in (1, 1000):    # sorted by one block, and by launches with the zeros beside them
+        out = torch.full((vocab, c), float("nan"), device="cuda")
+        dt = scv.embed_wgrad(ids.repeat(rows), dy.repeat(rows, 1), vocab, out=out)
+        have = torch.unique(ids).long()
+        slot = torch.searchsorted(have, ids.long())
+        ref, mag = (torch.zeros(len(have), c, dtype=torch.float64, device="cuda").index_add_(0, slot, rows * d)
+                    for d in (dy.double(), dy.double().abs()))
+        _within(dt[have], ref, (2 * rows + 2) * 2.0 ** -24 * mag, "gradient")
+        dt[have] = 0
+        assert not dt.any()
+        del out, dt
+
+
+def test_calls_without_rows():
+    """Nothing to do, and a gradient of zeros: no call refuses it."""
+    table, st = _rand(1, 20, 64, dtype=torch.bfloat16), scv.new_status()
+    none = table[:0]
+    ids = torch.empty(0, dtype=torch.int64, device="cuda")
+    assert scv.embed_fwd(ids, table, d_status=st).shape == (0, 64)
+    assert not scv.embed_wgrad(ids, none, 20, d_status=st).any()
+    f = scv.rms_norm_fwd(none, table[0].contiguous(), none.clone(), q8=True, q8_h=True)
+    assert f.y.shape == f.h.shape == f.y8.shape == f.h8.shape == (0, 64) and f.rstd.shape == (0,)
+    for h in (f.h, f.h8):
+        dx, dw = scv.rms_norm_bwd(none, h, f.rstd, table[0].contiguous())
+        assert dx.shape == (0, 64) and not dw.any()
+    assert scv.q8_unpack(scv.q8_pack(none)).shape == (0, 64)
+    scv.check_status(st)
+
+
 def test_refusal_of_tensors_that_are_not_contiguous():
     x = _rand(1, 8, 64)
     with pytest.raises(ValueError, match="contiguous"):
