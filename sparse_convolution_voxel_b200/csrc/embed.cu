@@ -19,8 +19,11 @@
 // other rows too.  Where these are many megabytes, a kernel of its own does, on a side stream,
 // while the sort and the sums, which wait for latencies more than for bandwidth, go on.
 //
-// A chain of three launches up to 4,096 rows, five to nine beyond: each takes 2 us and more, the
-// sums of 500k x 128 rows 30 us of the call's 55 (4.2 TB/s of random rows).
+// Launches: up to 4,096 rows (of 2^20 tokens at most) the sort, the sums and the join; beyond, the
+// bitmap's clear, a count and a scatter for every 10 bits of the vocabulary, with a scan between
+// them where the counts are many, the sums and the join; the zeros of a large table take one more.
+// So three to sixteen, of 2 us and more each.  500k x 128 bf16 rows of 1,000 tokens take 56 us with
+// six; the sums alone, one after the others, 33 (3.9 TB/s of random rows).
 #include <algorithm>
 
 #include "rows.cuh"
@@ -606,7 +609,7 @@ __global__ void __launch_bounds__(32 * kJoinRows) join_kernel(Runs p, int per_bl
 // Zeros for the tokens without rows, where the join does not store them.  A warp takes `tokens`
 // of them at a time (a power of two up to 32): each run of absent ones is a piece of the table
 // without a gap, written by bulk stores from a buffer of zeros.  (Stores from registers fill the
-// load and store units: 117 us for 32,768 rows x 512, 131,072 tokens, now 72.)
+// load and store units: for 32,768 rows x 512, 131,072 tokens, the call took 45 us more with them.)
 constexpr int kZeroThreads = 128, kZeroWarps = kZeroThreads / 32;
 constexpr uint32_t kZeroBytes = 16384;  // of the buffer
 __global__ void __launch_bounds__(kZeroThreads)
@@ -676,20 +679,23 @@ static int64_t tiles_of(int64_t n) {
 }
 
 // Up to this many counts (tiles x digit values) every block of the scatter scans them itself, a
-// launch less in every pass.  These calls wait for their launches: 8,192 rows of 1,000 tokens
-// 25 us, with the scan 28; 24,000 of 50,000 tokens 32, with it 38.  (On the GPU alone 32 tiles x
-// 1024 digit values take 2 us more so, 128 x 512 take 20.)  Beside a large table's zeros, whose
-// writes every read of a count waits behind, fewer: 32,768 rows x 512, 131,072 tokens (64 x 512
-// counts) 78 us, without the scan 121; 16,383 x 1024, 50,257 tokens (32 x 256) 64, without it 63.
+// launch less in every pass.  Where calls wait for their launches that is what counts: back to
+// back, 24,000 rows x 64 of 50,000 tokens (two passes of 47 x 256) take 38 us, with the scan 43.
+// Behind queued work, which hides the launches, the scatter's own scan costs a little: 40 us with
+// the scan's launch, 42 without; 16,384 x 64 of 1,000 tokens (32 x 1024) 29 and 33.  Beside a large
+// table's zeros, whose writes every read of a count waits behind, it costs more, so fewer there:
+// 32,768 rows x 512, 131,072 tokens (64 x 512 counts) 87 us with the scan, 125 without; 16,383 x
+// 1024, 50,257 tokens (32 x 256) 65 either way.
 constexpr int64_t kFewCounts = 32768, kFewCountsBeside = 8192;
 
 // Zeros of at least this many bytes have a kernel of their own: with the launches of a sort ahead
 // on the side stream (a fork and a join cost a few microseconds, the zeros of 16 MB as many);
 // behind a one-block sort in front of the sums, which are short.  (Beside those it came after the
 // sums' and the join's blocks had taken every SM, and crowded on the first that came free: 443 us
-// for 2,048 rows x 4096, 32,000 tokens, now 107.)
+// for 2,048 rows x 4096, 32,000 tokens, now 110.)
 constexpr size_t kLargeBytes = size_t(16) << 20;
-// (32,768 rows x 512, 131,072 tokens: 85 us with 74 blocks, 80 with 148, 75 with 296, 72 with 592 and more)
+// (32,768 rows x 512, 131,072 tokens: 103 us with 74 blocks, 107 with 148, 93 with 296, 87 with 592; 2,048 x 4096,
+// 32,000 tokens: 144, 134, 112 and 110)
 constexpr int kZeroBlocks = 592;
 constexpr int64_t kSmallWords = 32768;  // of the bitmap that the one-block sort clears itself
 

@@ -15,10 +15,12 @@
 //
 // The backward pass walks several rows per group.  A lane copies its slices of the rows ahead
 // with cp.async into a ring of its own in shared memory -- it alone reads them, so its own
-// copies are all it waits for -- which keeps some 150 KB per SM in flight without the
-// registers that loads ahead would take (500k x 128 bf16 from 8-bit rows, 450 MB: 98 us with
-// a row's loads in front of its work, 106 us with the next row in registers, 89 us so; 81 with
-// offsets that advance and two fp32 operations per instruction, of which 6 are dw's second kernel).
+// copies are all it waits for -- which keeps them in flight without the registers that loads
+// ahead would take: 160 KB per SM at 500k x 128 bf16 from 8-bit rows with dh (450 MB; back to back
+// on the same rows 98 us with a row's loads in front of its work, 106 us with the next row in
+// registers, 89 us so; 81 with offsets that advance and two fp32 operations per instruction, of
+// which 6 are dw's second kernel), less elsewhere: 37 KB at 1,032 channels of 16 bits, and at more
+// than 8,192 channels of fp32 no row ahead.
 //
 // dw: a fixed number of blocks (never more than there are row groups) walks the rows in
 // fixed steps with the sums of its rows in registers, adds its groups' sums in order in
@@ -135,7 +137,7 @@ template <typename T> struct Bwd {
     int c;
 };
 
-// Rows in the ring (the one at work included): what 200 KB of shared memory per SM admit.
+// Rows in the ring (the one at work included): within 200 KB of shared memory per SM for the widest rows of a form.
 template <typename T, int L, int K>
 constexpr int ring_rows() {
     return K == 4 && sizeof(T) == 4 ? 1 : K == 4 || sizeof(T) == 4 || (K == 2 && L == 0) ? 2 : 4;
@@ -161,7 +163,7 @@ constexpr size_t bwd_smem_limit() {
 }
 
 template <typename T, int L, int K>
-constexpr int min_blocks() {  // per SM, for the registers: what the ring admits
+constexpr int min_blocks() {  // per SM, for the registers
     return L > 0 && K == 1 ? 4 : L == 0 && K == 2 && sizeof(T) == 2 ? 2 : 1;
 }
 
@@ -411,7 +413,12 @@ static int rows_per_block(int c) {
     return slices <= 64 ? kThreads / l : 1;
 }
 
-// Blocks of the backward pass: as many as fit a B200's 148 SMs at once, by the ring.
+// Blocks of the backward pass, constants, so that the sums of dw depend on n and c alone: four on each of a B200's 148
+// SMs up to 256 channels and from 520 to 1,024, two up to 512, one above 8,192, which fit at once.  From 1,032 to 8,192
+// channels three, which fit up to 5,120 channels of 16 bits and 3,584 of fp32 (fewer with dh); wider rows take one and a
+// half to three waves.  With two instead (84 MB each of dy, h and dx, us): fp16 1,536 channels 109 -> 149, 2,048 90 -> 122, 4,096
+// 64 -> 78, 5,120 57 -> 74, but 8,192 67 -> 55; fp32 1,536 87 -> 89, but 2,048 89 -> 83, 4,096 77 -> 66, 5,120 78 -> 67,
+// 8,192 71 -> 69.
 static int64_t shares(int64_t n, int c) {
     const int64_t per = rows_per_block(c), most = c <= 256 ? 592 : c <= 512 ? 296 : c <= 1024 ? 592 : c <= 8192 ? 444 : 148;
     return std::max<int64_t>(1, std::min<int64_t>(most, (n + per - 1) / per));

@@ -23,7 +23,8 @@
 //     the A tile and the ring slot.  (It takes some 1,000 cycles a block: with one thread for
 //     both, that bounded maps whose rows lie in L2.)  Four warps store each segment's sum.
 // With the gathers in the widening warps, which then wait for one another's latencies, and
-// in shares of one piece, it took 76 us; now 65, of which the kernel's some 55 move 240 MB.
+// in shares of one piece, it took 76 us; now 64 back to back on the same rows, of which the kernel's
+// some 55 move 240 MB.
 //
 // The tensor cores cut bits off when they add: over thousands of pairs in one accumulator
 // that would be the largest error of the result (1.0e-6 of the norm at the size above, 5.5e-7
