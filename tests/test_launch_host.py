@@ -23,8 +23,13 @@ def fake(tmp_path_factory):
     at = tmp_path_factory.mktemp("fake")
     objs = [os.path.join(build.BUILD, f + ".cu.o") for f in ("embed", "norm")]
     subprocess.run(["gcc", "-O1", "-fPIC", "-c", os.path.join(HERE, "fake_cudart.c"), "-o", str(at / "fake.o")], check=True)
-    subprocess.run(["g++", "-shared", "-Wl,-Bsymbolic", "-Wl,--no-undefined", *objs, str(at / "fake.o"), "-o",
-                    str(at / "libfake.so")], check=True)
+    # nothing but the entry points is exported: inline functions' variables (a thread's side stream, the device's
+    # properties) would otherwise be one with those of the real library in this process
+    (at / "exports").write_text("{ global: lat_*; fake_*; local: *; };")
+    subprocess.run(["g++", "-shared", f"-Wl,--version-script={at / 'exports'}", "-Wl,--no-undefined", *objs,
+                    str(at / "fake.o"), "-o", str(at / "libfake.so")], check=True)
+    names = subprocess.run(["nm", "-D", "--defined-only", str(at / "libfake.so")], check=True, capture_output=True, text=True)
+    assert all(line.split()[-1].startswith(("lat_", "fake_")) for line in names.stdout.splitlines())
     lib = ctypes.CDLL(str(at / "libfake.so"))
     I32, I64, SZ, F = ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t, ctypes.c_float
     lib.lat_embed_wgrad_ws_bytes.restype, lib.lat_embed_wgrad_ws_bytes.argtypes = SZ, [I64, I64, I32]
