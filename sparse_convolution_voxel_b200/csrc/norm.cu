@@ -19,8 +19,8 @@
 // ahead would take: 160 KB per SM at 500k x 128 bf16 from 8-bit rows with dh (450 MB; back to back
 // on the same rows 98 us with a row's loads in front of its work, 106 us with the next row in
 // registers, 89 us so; 81 with offsets that advance and two fp32 operations per instruction, of
-// which 6 are dw's second kernel), less elsewhere: 37 KB at 1,032 channels of 16 bits, and at more
-// than 8,192 channels of fp32 no row ahead.
+// which 6 are dw's second kernel).  It is 28 KB at the least, at 1,032 channels of 16 bits from 8-bit
+// rows without dh, and above 8,192 channels of fp32 it holds no row ahead.
 //
 // dw: a fixed number of blocks (never more than there are row groups) walks the rows in
 // fixed steps with the sums of its rows in registers, adds its groups' sums in order in
@@ -416,9 +416,9 @@ static int rows_per_block(int c) {
 // Blocks of the backward pass, constants, so that the sums of dw depend on n and c alone: four on each of a B200's 148
 // SMs up to 256 channels and from 520 to 1,024, two up to 512, one above 8,192, which fit at once.  From 1,032 to 8,192
 // channels three, which fit up to 5,120 channels of 16 bits and 3,584 of fp32 (fewer with dh); wider rows take one and a
-// half to three waves.  With two instead (84 MB each of dy, h and dx, us): fp16 1,536 channels 109 -> 149, 2,048 90 -> 122, 4,096
-// 64 -> 78, 5,120 57 -> 74, but 8,192 67 -> 55; fp32 1,536 87 -> 89, but 2,048 89 -> 83, 4,096 77 -> 66, 5,120 78 -> 67,
-// 8,192 71 -> 69.
+// half to three waves.  With two instead (84 MB each of dy, h and dx, us): fp16 1,536 channels 109 -> 149, 2,048
+// 90 -> 122, 4,096 64 -> 78, 5,120 57 -> 74, but 8,192 67 -> 55; fp32 1,536 87 -> 89, but 2,048 89 -> 83, 4,096
+// 77 -> 66, 5,120 78 -> 67, 8,192 71 -> 69.
 static int64_t shares(int64_t n, int c) {
     const int64_t per = rows_per_block(c), most = c <= 256 ? 592 : c <= 512 ? 296 : c <= 1024 ? 592 : c <= 8192 ? 444 : 148;
     return std::max<int64_t>(1, std::min<int64_t>(most, (n + per - 1) / per));

@@ -32,7 +32,7 @@ constexpr int kTileM = 8;        // a thread's products: 8 input channels x 4 ou
 
 __host__ __device__ inline int pieces(int c) { return (c + kPiece - 1) / kPiece; }
 // Shares at most: the two blocks that each of a B200's 148 SMs holds (60,000 voxels, 305,000 pairs, 64 -> 64 fp32:
-// 91 us, with twice as many 96, with half 161).
+// 91 us, with twice as many 96, with half 114 and more).
 inline int most_shares(int cin, int cout) { return std::max(148, 296 / (pieces(cin) * pieces(cout))); }
 
 __device__ __forceinline__ int share_count(int64_t P, int most) {
